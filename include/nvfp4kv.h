@@ -118,9 +118,11 @@ nvfp4kv_status nvfp4kv_workspace_init(void* ws, size_t ws_bytes, nvfp4kv_stream_
 
 /* Synchronize `stream`, read the workspace's status word and clear it:
  * NVFP4KV_OK, NVFP4KV_ERR_DEVICE_TIMEOUT (a bounded wait inside a kernel gave
- * up), or NVFP4KV_ERR_UNSUPPORTED (an attention call met a key set whose V
+ * up), NVFP4KV_ERR_UNSUPPORTED (an attention call met a key set whose V
  * tensor scales span more than 2^116, beyond what its fp32 softmax sums hold;
- * that call's output is not valid).  A timeout outranks the other. */
+ * that call's output is not valid), or NVFP4KV_ERR_INVALID_ARG (a grouped
+ * product met offsets that decrease or leave [0, T]; that call wrote nothing).
+ * A timeout outranks the others, and the V scales outrank the offsets. */
 nvfp4kv_status nvfp4kv_workspace_status(void* ws, nvfp4kv_stream_t stream);
 
 /* ------------------------------------------------------------------ quantizer */
@@ -357,6 +359,88 @@ size_t nvfp4kv_matrix_workspace_bytes(void);
 nvfp4kv_status nvfp4kv_quantize_matrix(const void* X, int M, int N, int mode, void* codes,
                                        void* scales, float* tensor_scale, void* ws,
                                        nvfp4kv_stream_t stream);
+
+/* ------------------------------------------------------------------ matrix products */
+
+/* A quantized matrix as nvfp4kv_quantize_matrix writes it (device pointers):
+ * codes [R][K/2] and tensor_scale as there, scales [R][K/16]
+ * (NVFP4KV_BLOCKS_1D) or [R/16][K/16] (NVFP4KV_TILES_2D).  Codes and scales
+ * 16-byte aligned. */
+typedef struct {
+    const void* codes;
+    const void* scales;
+    const float* tensor_scale;
+    int mode;                /* nvfp4kv_block_shape */
+} nvfp4kv_matrix_view;
+
+typedef enum {
+    NVFP4KV_ACT_NONE = 0,
+    NVFP4KV_ACT_GELU_TANH = 1,   /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+    NVFP4KV_ACT_SILU = 2         /* z / (1 + exp(-z)) */
+} nvfp4kv_activation;
+
+/* What follows the product, in fp32, in this order; NULL leaves a part out. */
+typedef struct {
+    const float* bias;       /* [N], added to the product */
+    int activation;          /* nvfp4kv_activation */
+    const float* gate;       /* [ceil(M / rows_per_gate)][N], multiplies: row m
+                                takes gate row m / rows_per_gate (one gate per
+                                frame of a chunk) */
+    int rows_per_gate;       /* >= 1 where gate is given */
+    const void* residual;    /* [M][N] of Y's type, added last */
+    long long ld_residual;   /* elements between its rows, >= N */
+} nvfp4kv_epilogue;
+
+/*
+ * The product of a quantized activation matrix and a quantized weight matrix
+ * (DeepRead page, Method > 推理基础设施: W4A4 on Blackwell, FP4 GEMMs in place
+ * of BF16 ones), with its epilogue:
+ *   Y[m][n] = residual[m][n] + gate[m / rows_per_gate][n]
+ *             * act(s_X s_W sum_k x[m][k] w[n][k] + bias[n]),
+ * x, w the decoded codes times their block scales.
+ *   X: [M][K], W: [N][K]; each in either block shape.  K a multiple of 32,
+ *      and M (N) a multiple of 16 where X (W) is in tiles, else
+ *      NVFP4KV_ERR_UNSUPPORTED.
+ *   epilogue: NULL for none.
+ *   Y: [M][N] of y_dtype, ldy elements between rows (>= N).  Y may be the
+ *      residual itself (same address and stride); other overlaps of the two
+ *      are refused with NVFP4KV_ERR_INVALID_ARG.  Y must not overlap the other
+ *      inputs.
+ *   ws: a workspace of at least nvfp4kv_matrix_workspace_bytes(), initialized
+ *      once (nvfp4kv_quantize_matrix's serves; only its status word is used).
+ * Block products are summed by the tensor core in fp32; the epilogue is fp32;
+ * Y is rounded once.  Results do not depend on the stream or the run.  One
+ * launch; nothing is allocated.
+ */
+nvfp4kv_status nvfp4kv_matmul(const nvfp4kv_matrix_view* X, const nvfp4kv_matrix_view* W, int M,
+                              int N, int K, const nvfp4kv_epilogue* epilogue, void* Y,
+                              long long ldy, int y_dtype, void* ws, nvfp4kv_stream_t stream);
+
+/* Largest number of experts of one grouped product. */
+#define NVFP4KV_MAX_EXPERTS 1024
+
+/*
+ * The product grouped by expert: rows offsets[e] .. offsets[e + 1] - 1 of X
+ * times W_e, for E sets of weights (a text and a video modality in one packed
+ * sequence, or E experts with rows sorted by expert).
+ *   X: [T][K].  W: E matrices [N][K], stored one after the other: codes
+ *      [E][N][K/2], scales [E][N][K/16] or [E][N/16][K/16], tensor_scale [E].
+ *   offsets: int32 [E + 1], device, non-decreasing, in [0, T]; read by the
+ *      kernel (no synchronization).  Groups may be empty; rows outside
+ *      [offsets[0], offsets[E]) of Y are left as they are.  Offsets that
+ *      break the rule: nothing is written and nvfp4kv_workspace_status reports
+ *      NVFP4KV_ERR_INVALID_ARG.
+ *   epilogue: as nvfp4kv_matmul's, except bias [E][N] and gate [E][N] (row e
+ *      for group e; rows_per_gate is not read).
+ * E above NVFP4KV_MAX_EXPERTS: NVFP4KV_ERR_CAPACITY.  Otherwise as
+ * nvfp4kv_matmul.
+ */
+nvfp4kv_status nvfp4kv_grouped_matmul(const nvfp4kv_matrix_view* X, const nvfp4kv_matrix_view* W,
+                                      int E, int T, int N, int K, const int32_t* offsets,
+                                      const nvfp4kv_epilogue* epilogue, void* Y, long long ldy,
+                                      int y_dtype, void* ws, nvfp4kv_stream_t stream);
+
+/* ------------------------------------------------------------------ de-quantizer */
 
 /*
  * De-quantize a chunk back to [T_c][H][d] (device): x = decode(q) *

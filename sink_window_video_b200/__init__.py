@@ -45,6 +45,19 @@ class RopeView(ctypes.Structure):
                 ("rows", ctypes.c_int), ("cols", ctypes.c_int)]
 
 
+class MatrixView(ctypes.Structure):
+    """nvfp4kv_matrix_view: device pointers to one quantized matrix."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("tensor_scale", ctypes.c_void_p), ("mode", ctypes.c_int)]
+
+
+class Epilogue(ctypes.Structure):
+    """nvfp4kv_epilogue: what follows a matrix product."""
+    _fields_ = [("bias", ctypes.c_void_p), ("activation", ctypes.c_int),
+                ("gate", ctypes.c_void_p), ("rows_per_gate", ctypes.c_int),
+                ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_longlong)]
+
+
 class KVCacheConfig(ctypes.Structure):
     _fields_ = [("layers", ctypes.c_int), ("H", ctypes.c_int), ("d", ctypes.c_int),
                 ("T_c", ctypes.c_int), ("S_g", ctypes.c_int), ("S_s", ctypes.c_int),
@@ -66,6 +79,9 @@ def load():
     cv = ctypes.POINTER(ChunkView)
     cfgp = ctypes.POINTER(KVCacheConfig)
     rv = ctypes.POINTER(RopeView)
+    mv = ctypes.POINTER(MatrixView)
+    ep = ctypes.POINTER(Epilogue)
+    i64l = ctypes.c_longlong
     sigs = {
         "nvfp4kv_chunk_bytes": (sz, [i32, i32, i32]),
         "nvfp4kv_chunk_view_init": (st, [vp, i32, i32, i32, cv]),
@@ -96,6 +112,9 @@ def load():
         "nvfp4kv_tensor_scales_from_amax": (st, [vp, vp, vp]),
         "nvfp4kv_chunk_encode": (st, [vp, vp, i32, i32, i32, vp, vp, cv, vp]),
         "nvfp4kv_quantize_matrix": (st, [vp, i32, i32, i32, vp, vp, vp, vp, vp]),
+        "nvfp4kv_matmul": (st, [mv, mv, i32, i32, i32, ep, vp, i64l, i32, vp, vp]),
+        "nvfp4kv_grouped_matmul": (st, [mv, mv, i32, i32, i32, i32, vp, ep, vp, i64l, i32, vp,
+                                        vp]),
         "kvcache_pool_bytes": (sz, [cfgp]),
         "kvcache_create": (st, [cfgp, vp, vp, ctypes.POINTER(vp)]),
         "kvcache_destroy": (None, [vp]),
@@ -240,17 +259,30 @@ def chunk_encode(K, V, k_mean, tensor_scales, out: "ChunkBuffer", stream=None):
 BLOCKS_1D, TILES_2D = 1, 2
 
 
+def _check_part(t, shape, dtype, name):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {shape} tensor, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+
+
 class MatrixBuffer:
     """Device buffers of a quantized [M, N] matrix: codes [M, N/2] (uint8),
-    scales ([M, N/16] for 1D blocks, [M/16, N/16] for 2D tiles), tensor scale."""
+    scales ([M, N/16] for 1D blocks, [M/16, N/16] for 2D tiles), tensor scale.
+    `parts`: a (codes, scales, tensor_scale) that holds one already."""
 
-    def __init__(self, M, N, mode, device="cuda"):
+    def __init__(self, M, N, mode, device="cuda", parts=None):
         import torch
         self.M, self.N, self.mode = M, N, mode
         brows = M if mode == BLOCKS_1D else M // 16
-        self.codes = torch.zeros((M, N // 2), dtype=torch.uint8, device=device)
-        self.scales = torch.zeros((brows, N // 16), dtype=torch.uint8, device=device)
-        self.tensor_scale = torch.zeros(1, dtype=torch.float32, device=device)
+        shapes = (((M, N // 2), torch.uint8), ((brows, N // 16), torch.uint8),
+                  ((1,), torch.float32))
+        if parts is None:
+            parts = [torch.zeros(shape, dtype=dtype, device=device) for shape, dtype in shapes]
+        else:
+            for t, (shape, dtype), name in zip(parts, shapes, ("codes", "scales",
+                                                               "tensor_scale")):
+                _check_part(t, shape, dtype, name)
+        self.codes, self.scales, self.tensor_scale = parts
 
     def to_host(self):
         return dict(codes=self.codes.cpu().numpy(), scales=self.scales.cpu().numpy(),
@@ -273,6 +305,118 @@ def quantize_matrix(X, out: "MatrixBuffer", ws, stream=None):
                                           _ptr(out.scales), _ptr(out.tensor_scale), _ptr(ws),
                                           _stream(stream)),
            "nvfp4kv_quantize_matrix")
+
+
+class GroupedMatrixBuffer:
+    """Device buffers of E quantized [M, N] matrices, one after the other:
+    codes [E, M, N/2], scales [E, M or M/16, N/16], tensor_scale [E].
+    `parts`: a (codes, scales, tensor_scale) that holds them already."""
+
+    def __init__(self, E, M, N, mode, device="cuda", parts=None):
+        import torch
+        self.E, self.M, self.N, self.mode = E, M, N, mode
+        brows = M if mode == BLOCKS_1D else M // 16
+        shapes = (((E, M, N // 2), torch.uint8), ((E, brows, N // 16), torch.uint8),
+                  ((E,), torch.float32))
+        if parts is None:
+            parts = [torch.zeros(shape, dtype=dtype, device=device) for shape, dtype in shapes]
+        else:
+            for t, (shape, dtype), name in zip(parts, shapes, ("codes", "scales",
+                                                               "tensor_scale")):
+                _check_part(t, shape, dtype, name)
+        self.codes, self.scales, self.tensor_scale = parts
+
+    def expert(self, e) -> MatrixBuffer:
+        """Matrix e, for quantize_matrix to write."""
+        return MatrixBuffer(self.M, self.N, self.mode,
+                            parts=(self.codes[e], self.scales[e], self.tensor_scale[e:e + 1]))
+
+
+ACT_NONE, ACT_GELU_TANH, ACT_SILU = 0, 1, 2      # nvfp4kv_activation
+
+
+def _matrix_view(X):
+    return MatrixView(_ptr(X.codes), _ptr(X.scales), _ptr(X.tensor_scale), X.mode)
+
+
+def _rows(t, name, M, N, dtype=None):
+    """Row stride of a [M, N] tensor whose rows are contiguous."""
+    if t.dim() != 2 or tuple(t.shape) != (M, N) or (N > 1 and t.stride(1) != 1) or \
+            (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be a {dtype or ''} [{M}, {N}] tensor with contiguous "
+                         f"rows, got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
+    return t.stride(0) if M > 1 else max(N, t.stride(0))
+
+
+def _matmul_args(X, W, Y, bias, activation, gate, gate_rows, rows_per_gate, residual, lead, extra):
+    """Checks shared by the products; the epilogue and Y's row stride."""
+    import torch
+    M, N = X.M, W.M
+    if X.N != W.N:
+        raise ValueError(f"X has {X.N} columns and W {W.N}")
+    _dtype_code(Y)
+    ldy = _rows(Y, "Y", M, N)
+    ep = Epilogue(None, activation, None, rows_per_gate, None, 0)
+    if bias is not None:
+        _check_part(bias, lead + (N,), torch.float32, "bias")
+        ep.bias = _ptr(bias)
+    if gate is not None:
+        _check_part(gate, (gate_rows, N), torch.float32, "gate")
+        ep.gate = _ptr(gate)
+    if residual is not None:
+        ep.ld_residual = _rows(residual, "residual", M, N, Y.dtype)
+        ep.residual = _ptr(residual)
+    for t in (X.codes, X.scales, X.tensor_scale, W.codes, W.scales, W.tensor_scale, bias, gate,
+              residual) + extra:
+        if t is not None and t.device != Y.device:
+            raise ValueError(f"operands on {t.device} and {Y.device}")
+    return ep, ldy
+
+
+def _on_device_of(Y, stream, call):
+    """call(stream handle) with Y's device current; stream None is that
+    device's current stream."""
+    import torch
+    if Y.device.type != "cuda":
+        raise ValueError(f"Y is on {Y.device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(Y.device)
+    if torch.cuda.current_device() == Y.device.index:
+        return call(_stream(stream))
+    with torch.cuda.device(Y.device):
+        return call(_stream(stream))
+
+
+def matmul(X: "MatrixBuffer", W: "MatrixBuffer", Y, ws, bias=None, activation=ACT_NONE, gate=None,
+           rows_per_gate=0, residual=None, stream=None):
+    """Y = residual + gate * act(X W^T + bias) of quantized X [M, K] and
+    W [N, K] into Y [M, N] (float32 or bf16, contiguous rows, any row stride).
+    bias [N] float32; gate [ceil(M / rows_per_gate), N] float32, row m takes
+    gate row m // rows_per_gate; residual [M, N] of Y's dtype (may be Y)."""
+    if gate is not None and rows_per_gate < 1:
+        raise ValueError(f"rows_per_gate {rows_per_gate} with a gate")
+    gate_rows = -(-X.M // rows_per_gate) if gate is not None else 0
+    ep, ldy = _matmul_args(X, W, Y, bias, activation, gate, gate_rows, rows_per_gate, residual,
+                           (), (ws,))
+    xv, wv = _matrix_view(X), _matrix_view(W)
+    _check(_on_device_of(Y, stream, lambda s: load().nvfp4kv_matmul(
+        ctypes.byref(xv), ctypes.byref(wv), X.M, W.M, X.N, ctypes.byref(ep), _ptr(Y), ldy,
+        _dtype_code(Y), _ptr(ws), s)), "nvfp4kv_matmul")
+
+
+def grouped_matmul(X: "MatrixBuffer", W: "GroupedMatrixBuffer", offsets, Y, ws, bias=None,
+                   activation=ACT_NONE, gate=None, residual=None, stream=None):
+    """matmul by groups of rows: rows offsets[e] .. offsets[e + 1] - 1 of X
+    times matrix e of W; rows outside the groups of Y are left as they are.
+    offsets: int32 [E + 1] on the device; bias and gate [E, N] float32."""
+    import torch
+    _check_part(offsets, (W.E + 1,), torch.int32, "offsets")
+    ep, ldy = _matmul_args(X, W, Y, bias, activation, gate, W.E, 0, residual, (W.E,),
+                           (ws, offsets))
+    xv, wv = _matrix_view(X), _matrix_view(W)
+    _check(_on_device_of(Y, stream, lambda s: load().nvfp4kv_grouped_matmul(
+        ctypes.byref(xv), ctypes.byref(wv), W.E, X.M, W.M, X.N, _ptr(offsets), ctypes.byref(ep),
+        _ptr(Y), ldy, _dtype_code(Y), _ptr(ws), s)), "nvfp4kv_grouped_matmul")
 
 
 def attention_launches(n_chunks, T_c, H, T_q, d=HEAD_DIM) -> int:
@@ -298,8 +442,9 @@ def workspace_init(ws, stream=None):
 
 def workspace_status(ws, stream=None) -> int:
     """Synchronize and return the workspace status code and clear it: OK,
-    ERR_DEVICE_TIMEOUT (a bounded wait in a kernel gave up) or ERR_UNSUPPORTED
-    (an attention key set whose V tensor scales span more than 2^116)."""
+    ERR_DEVICE_TIMEOUT (a bounded wait in a kernel gave up), ERR_UNSUPPORTED
+    (an attention key set whose V tensor scales span more than 2^116) or
+    ERR_INVALID_ARG (a grouped product's offsets decrease or leave [0, T])."""
     return int(load().nvfp4kv_workspace_status(_ptr(ws), _stream(stream)))
 
 

@@ -148,6 +148,92 @@ nvfp4kv::RopeGeom rope_geom(const nvfp4kv_rope_view& r) {
     return g;
 }
 
+bool aligned_to(const void* p, unsigned n) {
+    return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
+// Whether two [M][N] matrices of `size`-byte elements share an element: their
+// address ranges are apart, or they lie side by side under one row stride.
+bool matrices_overlap(const void* A, long long lda, const void* B, long long ldb, int M, int N,
+                      int size) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(A), b = reinterpret_cast<uintptr_t>(B);
+    const uintptr_t na = ((uintptr_t)(M - 1) * lda + N) * size;
+    const uintptr_t nb = ((uintptr_t)(M - 1) * ldb + N) * size;
+    if (a + na <= b || b + nb <= a) return false;
+    if (lda != ldb) return true;
+    const uintptr_t row = (uintptr_t)lda * size, width = (uintptr_t)N * size;
+    const uintptr_t d = (a > b ? a - b : b - a) % row;
+    return d < width || row - d < width;
+}
+
+// The checks that both products share; rows of X and Y: M; E sets of weights.
+nvfp4kv_status check_matmul(const nvfp4kv_matrix_view* X, const nvfp4kv_matrix_view* W, int E,
+                            int M, int N, int K, const nvfp4kv_epilogue* ep, bool grouped,
+                            const void* Y, long long ldy, int y_dtype, const void* ws) {
+    constexpr int kMost = 1 << 24;
+    if (!X || !W || !Y || !ws || !X->codes || !X->scales || !X->tensor_scale || !W->codes ||
+        !W->scales || !W->tensor_scale || M <= 0 || N <= 0 || K <= 0 || E <= 0 || M > kMost ||
+        N > kMost || K > kMost || (long long)M * K > (1ll << 34) ||
+        (long long)N * K > (1ll << 34) || (long long)M * N > (1ll << 34) || ldy < N || ldy > (1ll << 40) ||
+        (y_dtype != NVFP4KV_F32 && y_dtype != NVFP4KV_BF16))
+        return NVFP4KV_ERR_INVALID_ARG;
+    for (const nvfp4kv_matrix_view* v : {X, W})
+        if (v->mode != NVFP4KV_BLOCKS_1D && v->mode != NVFP4KV_TILES_2D)
+            return NVFP4KV_ERR_INVALID_ARG;
+    const int size = y_dtype == NVFP4KV_F32 ? 4 : 2;
+    if (ep) {
+        if (ep->activation < NVFP4KV_ACT_NONE || ep->activation > NVFP4KV_ACT_SILU ||
+            (ep->gate && !grouped && ep->rows_per_gate < 1) ||
+            (ep->residual && (ep->ld_residual < N || ep->ld_residual > (1ll << 40))))
+            return NVFP4KV_ERR_INVALID_ARG;
+        if (ep->residual && !(ep->residual == Y && ep->ld_residual == ldy) &&
+            matrices_overlap(Y, ldy, ep->residual, ep->ld_residual, M, N, size))
+            return NVFP4KV_ERR_INVALID_ARG;
+    }
+    if (E > NVFP4KV_MAX_EXPERTS) return NVFP4KV_ERR_CAPACITY;
+    if (K % 32 != 0 || (X->mode == NVFP4KV_TILES_2D && M % 16 != 0) ||
+        (W->mode == NVFP4KV_TILES_2D && N % 16 != 0))
+        return NVFP4KV_ERR_UNSUPPORTED;
+    if (!aligned16(X->codes) || !aligned16(X->scales) || !aligned16(W->codes) ||
+        !aligned16(W->scales) || !aligned_to(X->tensor_scale, 4) ||
+        !aligned_to(W->tensor_scale, 4) || !aligned_to(Y, size) || !aligned256(ws) ||
+        (ep && (!aligned_to(ep->bias, 4) || !aligned_to(ep->gate, 4) ||
+                !aligned_to(ep->residual, size))))
+        return NVFP4KV_ERR_ALIGNMENT;
+    return have_sm100() ? NVFP4KV_OK : NVFP4KV_ERR_UNSUPPORTED;
+}
+
+nvfp4kv_status run_matmul(const nvfp4kv_matrix_view& X, const nvfp4kv_matrix_view& W, int E, int M,
+                          int N, int K, const int32_t* offsets, const nvfp4kv_epilogue* ep,
+                          void* Y, long long ldy, int y_dtype, void* ws, nvfp4kv_stream_t stream) {
+    nvfp4kv::MatmulArgs a = {};
+    a.x_scales = static_cast<const uint8_t*>(X.scales);
+    a.w_scales = static_cast<const uint8_t*>(W.scales);
+    a.x_scale = X.tensor_scale;
+    a.w_scale = W.tensor_scale;
+    a.x_shift = X.mode == NVFP4KV_TILES_2D ? 4 : 0;
+    a.w_shift = W.mode == NVFP4KV_TILES_2D ? 4 : 0;
+    a.w_scale_rows = N >> a.w_shift;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.E = E;
+    a.offsets = offsets;
+    if (ep) {
+        a.bias = ep->bias;
+        a.gate = ep->gate;
+        a.rows_per_gate = ep->rows_per_gate;
+        a.act = ep->activation;
+        a.residual = ep->residual;
+        a.ldr = ep->ld_residual;
+    }
+    a.Y = Y;
+    a.ldy = ldy;
+    a.y_f32 = y_dtype == NVFP4KV_F32 ? 1 : 0;
+    a.ctl = static_cast<nvfp4kv::Control*>(ws);
+    return nvfp4kv::launch_matmul(a, W.codes, X.codes, (cudaStream_t)stream);
+}
+
 }  // namespace
 
 namespace nvfp4kv {
@@ -219,8 +305,10 @@ nvfp4kv_status nvfp4kv_workspace_status(void* ws, nvfp4kv_stream_t stream) {
     if (cudaMemsetAsync(ws, 0, sizeof(unsigned), s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
         return NVFP4KV_ERR_CUDA;
-    // a wait that gave up outranks an input the attention could not represent
-    return (st & 1u) ? NVFP4KV_ERR_DEVICE_TIMEOUT : NVFP4KV_ERR_UNSUPPORTED;
+    // a wait that gave up outranks an input the attention could not represent,
+    // and that outranks a grouped product's offsets
+    if (st & 1u) return NVFP4KV_ERR_DEVICE_TIMEOUT;
+    return (st & 2u) ? NVFP4KV_ERR_UNSUPPORTED : NVFP4KV_ERR_INVALID_ARG;
 }
 
 nvfp4kv_status nvfp4kv_quantize_chunk(const void* K, const void* V, int T_c, int H, int d,
@@ -363,6 +451,26 @@ nvfp4kv_status nvfp4kv_quantize_matrix(const void* X, int M, int N, int mode, vo
     if (!have_sm100()) return NVFP4KV_ERR_UNSUPPORTED;
     return launch_quantize_matrix(X, M, N, mode, codes, scales, tensor_scale, ws,
                                   (cudaStream_t)stream);
+}
+
+nvfp4kv_status nvfp4kv_matmul(const nvfp4kv_matrix_view* X, const nvfp4kv_matrix_view* W, int M,
+                              int N, int K, const nvfp4kv_epilogue* epilogue, void* Y,
+                              long long ldy, int y_dtype, void* ws, nvfp4kv_stream_t stream) {
+    const nvfp4kv_status st =
+        check_matmul(X, W, 1, M, N, K, epilogue, false, Y, ldy, y_dtype, ws);
+    if (st != NVFP4KV_OK) return st;
+    return run_matmul(*X, *W, 1, M, N, K, nullptr, epilogue, Y, ldy, y_dtype, ws, stream);
+}
+
+nvfp4kv_status nvfp4kv_grouped_matmul(const nvfp4kv_matrix_view* X, const nvfp4kv_matrix_view* W,
+                                      int E, int T, int N, int K, const int32_t* offsets,
+                                      const nvfp4kv_epilogue* epilogue, void* Y, long long ldy,
+                                      int y_dtype, void* ws, nvfp4kv_stream_t stream) {
+    if (!offsets) return NVFP4KV_ERR_INVALID_ARG;
+    const nvfp4kv_status st = check_matmul(X, W, E, T, N, K, epilogue, true, Y, ldy, y_dtype, ws);
+    if (st != NVFP4KV_OK) return st;
+    if (!aligned_to(offsets, 4)) return NVFP4KV_ERR_ALIGNMENT;
+    return run_matmul(*X, *W, E, T, N, K, offsets, epilogue, Y, ldy, y_dtype, ws, stream);
 }
 
 nvfp4kv_status nvfp4kv_dequantize(const nvfp4kv_chunk_view* in, int T_c, int H, int d,

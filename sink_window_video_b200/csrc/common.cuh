@@ -20,6 +20,7 @@ constexpr float kTensorScaleDiv = 2688.0f;   // 6 * 448
 // Status bits recorded by kernels in the workspace.
 constexpr unsigned kStatusTimeout = 1u;
 constexpr unsigned kStatusRange = 2u;   // attention: key set's V scales span more than 2^116
+constexpr unsigned kStatusOffsets = 4u; // grouped product: offsets that decrease or leave [0, T]
 
 // Time limit of any single wait inside a kernel, in nanoseconds; a wait that
 // reaches it records kStatusTimeout (and its site) and the kernel returns.

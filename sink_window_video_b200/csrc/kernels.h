@@ -119,6 +119,32 @@ nvfp4kv_status launch_quantize_matrix(const void* X, int M, int N, int mode, voi
                                       void* scales, float* tensor_scale, void* ws,
                                       cudaStream_t stream);
 
+// Products of NVFP4 matrices (matmul.cu): Y = R + g * act(s_X s_W X W^T + b).
+// Dense (offsets null) or rows [offsets[e], offsets[e + 1]) of X times expert
+// e's weights.
+constexpr int kMaxExperts = 1024;
+struct MatmulArgs {
+    const uint8_t* x_scales;     // E4M3 block scales [ceil rows >> x_shift][K / 16]
+    const uint8_t* w_scales;     // [E][w_scale_rows][K / 16]
+    const float* x_scale;        // s_X
+    const float* w_scale;        // s_W [E]
+    int x_shift, w_shift;        // rows per scale row: 1 << shift (0 or 4)
+    int w_scale_rows;
+    int M, N, K, E;
+    const int* offsets;          // device [E + 1], or null
+    const float* bias;           // [E][N] or null
+    const float* gate;           // [ceil(M / rows_per_gate)][N] (grouped: [E][N]) or null
+    int rows_per_gate;
+    int act;                     // nvfp4kv_activation
+    const void* residual;        // Y's type, row stride ldr, or null
+    void* Y;
+    int y_f32;
+    long long ldr, ldy;
+    struct Control* ctl;
+};
+nvfp4kv_status launch_matmul(const MatmulArgs& a, const void* w_codes, const void* x_codes,
+                             cudaStream_t stream);
+
 // 3D rotary position embedding (rope.cu): a chunk's cos/sin table and the
 // frame grid of its tokens (frames * rows * cols >= T).
 struct RopeGeom {

@@ -1,0 +1,525 @@
+// matmul.cu -- products of NVFP4 matrices on the block-scaled FP4 tensor cores
+// (tcgen05.mma kind::mxf4nvf4), with the epilogue fused, dense and grouped by
+// expert:
+//   Y[m][n] = R[m][n] + g * act(s_X s_W sum_k x[m][k] w[n][k] + b[n]),
+// x and w the E2M1 codes times their E4M3 block scales (16 elements along k).
+//
+// The tensor core's A operand is the WEIGHT tile (128 output channels) and B
+// the token tile (TN rows of X): a tensor-memory lane is then an output
+// channel and a column a token, so one kernel serves one token and thousands
+// (the token count only sets the instruction's N), a thread's bias is one
+// register, and the 32 lanes of a warp store 32 neighbouring channels of one
+// row of Y.
+//
+// One persistent CTA per SM over a static tile list; roles by warp:
+//   warps 0-3  block scales: global -> registers (a stage ahead) -> shared
+//              memory in the tensor core's scale layout (below)
+//   warps 4-7  epilogue: tensor memory -> registers -> Y
+//   warp 8     TMA loads of both code tiles (lane 0)
+//   warp 9     tcgen05.cp of the scales into tensor memory and the MMAs (lane 0)
+// A stage holds 256 elements along k: 128 bytes of codes a row (one 128-byte
+// swizzle row) and 16 scale bytes a row.  Two accumulators in tensor memory
+// let the epilogue of one tile run under the next tile's MMAs.
+// Scale layout of one K = 64 step and 128 rows: 512 bytes, row r's four block
+// scales (bytes) at (r % 32) * 16 + (r / 32) * 4, which tcgen05.cp
+// (32x128b.warpx4) places in 4 columns of every lane quarter.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_ptx.cuh"
+
+namespace nvfp4kv {
+using namespace tc;
+namespace {
+
+constexpr int kTileN = 128;                 // output channels of a tile (the MMA's M)
+constexpr int kStageK = 256;                // elements along k of one stage
+constexpr int kThreadsMM = 320;
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kColsMM = 512;                // tensor-memory columns
+constexpr uint32_t kColSFAm = 448, kColSFBm = 464;   // 16 and 32 columns
+constexpr int kATile = kTileN * 128;        // bytes of codes of a weight tile's stage
+constexpr int kSfaBytes = 4 * 512;
+constexpr int kMaxStages = 12;
+
+template <int TN>
+struct Shape {
+    static constexpr int kBTile = TN * 128;
+    static constexpr int kSfbBytes = 4 * 512 * ((TN + 127) / 128);
+    static constexpr int kStage = kATile + kBTile + kSfaBytes + kSfbBytes;
+    static constexpr int kStages = (200 * 1024) / kStage < kMaxStages ? (200 * 1024) / kStage
+                                                                      : kMaxStages;
+    static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+    static_assert(kStage % 1024 == 0, "stages keep the swizzle alignment");
+    static_assert(2 * TN <= (int)kColSFAm, "two accumulators beside the scales");
+};
+
+struct MMShared {
+    uint64_t tma_full[kMaxStages];
+    uint64_t sf_full[kMaxStages];
+    uint64_t empty[kMaxStages];
+    uint64_t acc_full[2];
+    uint64_t acc_free[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    int bad_offsets;
+};
+
+__device__ __forceinline__ bool wait_or_abort_m(uint32_t mbar, uint32_t parity, volatile int* abort,
+                                                Control* ctl, unsigned site, unsigned step) {
+    if (mbar_try_wait(mbar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i)
+            if (mbar_try_wait(mbar, parity)) return true;
+        if (*abort) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            record_timeout(ctl, site, step, parity);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(mbar)
+        : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect_tx(uint32_t mbar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mbar), "r"(bytes)
+                 : "memory");
+}
+
+// 512 bytes (32 rows of 16) of shared memory into 4 columns of all four lane
+// quarters.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t tmem, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc));
+}
+
+// Four consecutive block scales of one row from byte kb of it (zeros from
+// byte kbytes on).  kbytes is even (K a multiple of 32).
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int kb, int kbytes) {
+    const int left = kbytes - kb;
+    if (left <= 0) return 0u;
+    if ((kbytes & 3) == 0) return __ldg(reinterpret_cast<const uint32_t*>(row + kb));
+    const uint32_t lo = __ldg(reinterpret_cast<const uint16_t*>(row + kb));
+    const uint32_t hi = left > 2 ? __ldg(reinterpret_cast<const uint16_t*>(row + kb + 2)) : 0u;
+    return lo | (hi << 16);
+}
+
+// The 16 block scales of one stage of one row.
+__device__ __forceinline__ uint4 scale_row(const uint8_t* row, int kb, int kbytes) {
+    if ((kbytes & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(row + kb));
+    return make_uint4(scale_word(row, kb, kbytes), scale_word(row, kb + 4, kbytes),
+                      scale_word(row, kb + 8, kbytes), scale_word(row, kb + 12, kbytes));
+}
+
+__device__ __forceinline__ float act_apply(float z, int act) {
+    if (act == NVFP4KV_ACT_NONE) return z;
+    // z * sigmoid(v): v = z (SiLU), or 2 sqrt(2/pi) (z + 0.044715 z^3) (GELU, tanh form)
+    const float v = act == NVFP4KV_ACT_SILU
+                        ? z
+                        : 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);
+    return __fdividef(z, 1.0f + ex2f(-1.4426950408889634f * v));
+}
+
+struct TileAt {
+    int e, n0, m0, m_end;
+};
+
+template <int TN, bool kGrouped>
+struct Tiles {
+    const MatmulArgs& a;
+    const int* s_off;
+    const int* s_tile;
+    int n_tiles, e;
+    __device__ Tiles(const MatmulArgs& args, const int* off, const int* tile)
+        : a(args), s_off(off), s_tile(tile), e(0) {
+        n_tiles = (a.N + kTileN - 1) / kTileN;
+    }
+    __device__ int total() const {
+        return kGrouped ? s_tile[a.E] : ((a.M + TN - 1) / TN) * n_tiles;
+    }
+    // t grows from call to call
+    __device__ TileAt at(int t) {
+        TileAt r;
+        int row0 = 0, m_end = a.M;
+        if (kGrouped) {
+            while (s_tile[e + 1] <= t) ++e;
+            t -= s_tile[e];
+            row0 = s_off[e];
+            m_end = s_off[e + 1];
+        }
+        const int mt = t / n_tiles;
+        r.e = e;
+        r.n0 = (t - mt * n_tiles) * kTileN;
+        r.m0 = row0 + mt * TN;
+        r.m_end = min(m_end, r.m0 + TN);
+        return r;
+    }
+};
+
+template <int TN, bool kGrouped>
+__global__ void __launch_bounds__(kThreadsMM, 1)
+matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+              const MatmulArgs a) {
+    using S = Shape<TN>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ MMShared sh;
+    __shared__ int s_off[kGrouped ? kMaxExperts + 1 : 1];
+    __shared__ int s_tile[kGrouped ? kMaxExperts + 1 : 1];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int* abort = &sh.abort;
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&sh.tmem_base)),
+                     "r"(kColsMM));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (tid == 0) {
+        sh.abort = 0;
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(smem_u32(&sh.tma_full[s]), 1);
+            mbar_init(smem_u32(&sh.sf_full[s]), 4);
+            mbar_init(smem_u32(&sh.empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.acc_full[i]), 1);
+            mbar_init(smem_u32(&sh.acc_free[i]), 4);
+        }
+        mbar_init(smem_u32(&sh.drain), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (kGrouped && warp == 0) {
+        // tile count prefix over the experts; offsets that decrease or leave
+        // [0, M] are reported and nothing is computed
+        const int nt = (a.N + kTileN - 1) / kTileN;
+        int carry = 0;
+        bool bad = false;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane;
+            int cnt = 0;
+            if (e < a.E) {
+                const int o0 = a.offsets[e], o1 = a.offsets[e + 1];
+                bad |= o0 < 0 || o1 < o0 || o1 > a.M;
+                s_off[e] = o0;
+                if (e == a.E - 1) s_off[a.E] = o1;
+                cnt = ((o1 - o0 + TN - 1) / TN) * nt;
+            }
+            int inc = cnt;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+                if (lane >= d) inc += v;
+            }
+            if (e < a.E) s_tile[e + 1] = carry + inc;
+            carry += __shfl_sync(0xFFFFFFFFu, inc, 31);
+        }
+        bad = __any_sync(0xFFFFFFFFu, bad);
+        if (lane == 0) {
+            s_tile[0] = 0;
+            if (bad) {
+                s_tile[a.E] = 0;
+                if (blockIdx.x == 0) atomicOr(&a.ctl->status, kStatusOffsets);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem_base;
+    Tiles<TN, kGrouped> tiles(a, s_off, s_tile);
+    const int total = tiles.total();
+    const int steps = (a.K + kStageK - 1) / kStageK;
+    const int kbytes = a.K / 16;
+
+    if (warp < 4) {
+        // ------------------------------------------------------------ block scales
+        // thread = row of each 128-row group: 16 bytes of the weight row and of
+        // TN / 128 token rows per stage, loaded one stage ahead
+        constexpr int kRows = (TN + 127) / 128;
+        const bool withhold = blockIdx.x == 0 && warp == 0 && (a.ctl->test_flags & 1u) != 0u;
+        const uint32_t line = (uint32_t)(lane * 16 + warp * 4);
+        uint4 wv, xv[kRows];
+        TileAt cur;
+        auto load = [&](int t, int s) {
+            if (s == 0) cur = tiles.at(t);
+            const int n = cur.n0 + tid;
+            wv = make_uint4(0u, 0u, 0u, 0u);
+            if (n < a.N)
+                wv = scale_row(a.w_scales + ((size_t)cur.e * a.w_scale_rows + (n >> a.w_shift)) *
+                                                kbytes,
+                               s * 16, kbytes);
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int r = 128 * i + tid, m = cur.m0 + r;
+                xv[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < TN && m < cur.m_end)
+                    xv[i] = scale_row(a.x_scales + (size_t)(m >> a.x_shift) * kbytes, s * 16, kbytes);
+            }
+        };
+        auto put = [&](uint8_t* dst, const uint4& v, int stride) {
+            *reinterpret_cast<uint32_t*>(dst + line) = v.x;
+            *reinterpret_cast<uint32_t*>(dst + line + stride) = v.y;
+            *reinterpret_cast<uint32_t*>(dst + line + 2 * stride) = v.z;
+            *reinterpret_cast<uint32_t*>(dst + line + 3 * stride) = v.w;
+        };
+        int it = 0;
+        bool ok = true;
+        if ((int)blockIdx.x < total) load(blockIdx.x, 0);
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            for (int s = 0; s < steps; ++s, ++it) {
+                const int st = it % S::kStages;
+                if (it >= S::kStages) {
+                    ok = wait_or_abort_m(smem_u32(&sh.empty[st]),
+                                         (uint32_t)((it / S::kStages - 1) & 1), abort, a.ctl, 60u, it);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                }
+                uint8_t* sf = base + (size_t)st * S::kStage + kATile + S::kBTile;
+                put(sf, wv, 512);
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) put(sf + kSfaBytes + 512 * i, xv[i], 512 * kRows);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0 && !(withhold && it == 0)) mbar_arrive(smem_u32(&sh.sf_full[st]));
+                if (s + 1 < steps) load(t, s + 1);
+                else if (t + (int)gridDim.x < total) load(t + gridDim.x, 0);
+            }
+        }
+    } else if (warp < 8) {
+        // ------------------------------------------------------------ epilogue
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        int i = 0;
+        for (int t = blockIdx.x; t < total; t += gridDim.x, ++i) {
+            const TileAt at = tiles.at(t);
+            const int buf = i & 1;
+            bool got = wait_or_abort_m(smem_u32(&sh.acc_full[buf]), (uint32_t)((i >> 1) & 1), abort,
+                                       a.ctl, 61u, i);
+            if (!__all_sync(0xFFFFFFFFu, got)) break;
+            tc_fence_after();
+            const int n = at.n0 + (warp & 3) * 32 + lane;
+            const bool nv = n < a.N;
+            const size_t en = (size_t)at.e * a.N + n;
+            const float alpha = __ldg(a.x_scale) * __ldg(a.w_scale + at.e);
+            const float b = (a.bias && nv) ? __ldg(a.bias + en) : 0.0f;
+            float g = (a.gate && kGrouped && nv) ? __ldg(a.gate + en) : 1.0f;
+#pragma unroll 1
+            for (int c = 0; c < TN && at.m0 + c < at.m_end; c += 16) {
+                uint32_t v[16];
+                tmem_ld16(tmem + lane_base + (uint32_t)(buf * TN + c), v);
+                tmem_wait_ld();
+                if (nv) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int m = at.m0 + c + j;
+                        if (m < at.m_end) {
+                            float z = act_apply(fmaf(__uint_as_float(v[j]), alpha, b), a.act);
+                            if (!kGrouped && a.gate)
+                                g = __ldg(a.gate + (size_t)(m / a.rows_per_gate) * a.N + n);
+                            if (a.gate) z *= g;
+                            if (a.y_f32) {
+                                if (a.residual)
+                                    z += static_cast<const float*>(a.residual)[(size_t)m * a.ldr + n];
+                                static_cast<float*>(a.Y)[(size_t)m * a.ldy + n] = z;
+                            } else {
+                                if (a.residual)
+                                    z += __bfloat162float(static_cast<const __nv_bfloat16*>(
+                                        a.residual)[(size_t)m * a.ldr + n]);
+                                static_cast<__nv_bfloat16*>(a.Y)[(size_t)m * a.ldy + n] =
+                                    __float2bfloat16_rn(z);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.acc_free[buf]));
+        }
+    } else if (warp == kTmaWarp) {
+        // ------------------------------------------------------------ code tiles
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                const TileAt at = tiles.at(t);
+                for (int s = 0; s < steps; ++s, ++it) {
+                    const int st = it % S::kStages;
+                    if (it >= S::kStages) {
+                        ok = wait_or_abort_m(smem_u32(&sh.empty[st]),
+                                             (uint32_t)((it / S::kStages - 1) & 1), abort, a.ctl, 62u,
+                                             it);
+                        if (!ok) break;
+                    }
+                    const uint32_t dst = smem_u32(base + (size_t)st * S::kStage);
+                    const uint32_t bar = smem_u32(&sh.tma_full[st]);
+                    mbar_expect_tx(bar, (uint32_t)(kATile + S::kBTile));
+                    tma_load_3d(dst, &map_w, s * 128, at.n0, at.e, bar);
+                    tma_load_3d(dst + kATile, &map_x, s * 128, at.m0, 0, bar);
+                }
+            }
+            if (!ok) {
+                // the loads in flight land before the CTA leaves
+                const int first = it > S::kStages ? it - S::kStages : 0;
+                for (int i = first; i < it; ++i)
+                    mbar_wait(smem_u32(&sh.tma_full[i % S::kStages]),
+                              (uint32_t)((i / S::kStages) & 1));
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ MMA issue
+        if (lane == 0) {
+            constexpr uint32_t idesc = umma_idesc_fp4(TN);
+            constexpr int kSfbGroups = (TN + 127) / 128;
+            int it = 0, i = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++i) {
+                const int buf = i & 1;
+                if (i >= 2) {
+                    ok = wait_or_abort_m(smem_u32(&sh.acc_free[buf]), (uint32_t)((i / 2 - 1) & 1),
+                                         abort, a.ctl, 63u, i);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                const uint32_t d = tmem + (uint32_t)(buf * TN);
+                for (int s = 0; s < steps; ++s, ++it) {
+                    const int st = it % S::kStages;
+                    const uint32_t par = (uint32_t)((it / S::kStages) & 1);
+                    ok = wait_or_abort_m(smem_u32(&sh.sf_full[st]), par, abort, a.ctl, 64u, it) &&
+                         wait_or_abort_m(smem_u32(&sh.tma_full[st]), par, abort, a.ctl, 65u, it);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(base + (size_t)st * S::kStage);
+                    const uint32_t sf = sa + kATile + S::kBTile;
+                    const uint64_t da = umma_desc(sa, 16, 1024);
+                    const uint64_t db = umma_desc(sa + kATile, 16, 1024);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        tmem_cp_scales(tmem + kColSFAm + 4u * j,
+                                       umma_desc_noswizzle(sf + 512 * j, 16, 128));
+#pragma unroll
+                        for (int q = 0; q < kSfbGroups; ++q)
+                            tmem_cp_scales(tmem + kColSFBm + 8u * j + 4u * q,
+                                           umma_desc_noswizzle(
+                                               sf + kSfaBytes + 512 * (kSfbGroups * j + q), 16, 128));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_fp4(d, da + 2u * j, db + 2u * j, idesc, (s | j) ? 1u : 0u,
+                                tmem + kColSFAm + 4u * j, tmem + kColSFBm + 8u * j);
+                    mma_commit(smem_u32(&sh.empty[st]));
+                }
+                if (ok) mma_commit(smem_u32(&sh.acc_full[buf]));
+            }
+            mma_commit(smem_u32(&sh.drain));
+            mbar_wait(smem_u32(&sh.drain), 0u);
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kColsMM));
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// Codes [depth][rows][K / 2] as bytes, tiles of `box` rows of 128 bytes with
+// the 128-byte swizzle; what lies outside reads as zero codes.
+bool make_map(CUtensorMap* map, const void* codes, int K, int rows, int depth, int box) {
+    const EncodeTiled fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)K / 2, (cuuint64_t)rows, (cuuint64_t)depth};
+    const cuuint64_t strides[2] = {(cuuint64_t)K / 2, (cuuint64_t)K / 2 * rows};
+    const cuuint32_t boxes[3] = {128, (cuuint32_t)box, 1};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides, boxes,
+              ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count_of(int dev) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return n;
+}
+
+template <int TN, bool kGrouped>
+nvfp4kv_status launch_tn(const MatmulArgs& a, const void* w_codes, const void* x_codes,
+                         cudaStream_t stream) {
+    CUtensorMap map_w, map_x;
+    if (!make_map(&map_w, w_codes, a.K, a.N, kGrouped ? a.E : 1, kTileN) ||
+        !make_map(&map_x, x_codes, a.K, a.M, 1, TN))
+        return NVFP4KV_ERR_CUDA;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4KV_ERR_CUDA;
+    if (cudaFuncSetAttribute(matmul_kernel<TN, kGrouped>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)Shape<TN>::kSmem) != cudaSuccess)
+        return NVFP4KV_ERR_CUDA;
+    const long long n_tiles = (a.N + kTileN - 1) / kTileN;
+    // grouped: at most one more token tile per expert than the rows fill
+    const long long most = n_tiles * ((a.M + TN - 1) / TN + (kGrouped ? a.E : 0));
+    const int sms = sm_count_of(dev);
+    const int grid = (int)(most < sms ? most : sms);
+    if (grid <= 0) return NVFP4KV_ERR_CUDA;
+    matmul_kernel<TN, kGrouped><<<grid, kThreadsMM, Shape<TN>::kSmem, stream>>>(map_w, map_x, a);
+    return cudaGetLastError() == cudaSuccess ? NVFP4KV_OK : NVFP4KV_ERR_CUDA;
+}
+
+template <bool kGrouped>
+nvfp4kv_status launch_any(const MatmulArgs& a, const void* w_codes, const void* x_codes,
+                          cudaStream_t stream) {
+    const int per = kGrouped ? (a.M + a.E - 1) / a.E : a.M;
+    if (per <= 32) return launch_tn<32, kGrouped>(a, w_codes, x_codes, stream);
+    if (per <= 128) return launch_tn<128, kGrouped>(a, w_codes, x_codes, stream);
+    return launch_tn<192, kGrouped>(a, w_codes, x_codes, stream);
+}
+
+}  // namespace
+
+nvfp4kv_status launch_matmul(const MatmulArgs& a, const void* w_codes, const void* x_codes,
+                             cudaStream_t stream) {
+    return a.offsets ? launch_any<true>(a, w_codes, x_codes, stream)
+                     : launch_any<false>(a, w_codes, x_codes, stream);
+}
+
+}  // namespace nvfp4kv

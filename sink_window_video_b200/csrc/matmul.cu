@@ -14,9 +14,9 @@
 // One persistent CTA per SM over a static tile list; roles by warp:
 //   warps 0-3  block scales: global -> registers (a stage ahead) -> shared
 //              memory in the tensor core's scale layout (below)
-//   warps 4-7  epilogue: tensor memory -> registers -> Y
-//   warp 8     TMA loads of both code tiles (lane 0)
-//   warp 9     tcgen05.cp of the scales into tensor memory and the MMAs (lane 0)
+//   warps 4-11 epilogue: tensor memory -> registers -> Y
+//   warp 12    TMA loads of both code tiles (lane 0)
+//   warp 13    tcgen05.cp of the scales into tensor memory and the MMAs (lane 0)
 // A stage holds 256 elements along k: 128 bytes of codes a row (one 128-byte
 // swizzle row) and 16 scale bytes a row.  Two accumulators in tensor memory
 // let the epilogue of one tile run under the next tile's MMAs.
@@ -35,8 +35,8 @@ namespace {
 
 constexpr int kTileN = 128;                 // output channels of a tile (the MMA's M)
 constexpr int kStageK = 256;                // elements along k of one stage
-constexpr int kThreadsMM = 320;
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kThreadsMM = 448;
+constexpr int kTmaWarp = 12, kMmaWarp = 13;
 constexpr int kColsMM = 512;                // tensor-memory columns
 constexpr uint32_t kColSFAm = 448, kColSFBm = 464;   // 16 and 32 columns
 constexpr int kATile = kTileN * 128;        // bytes of codes of a weight tile's stage
@@ -122,13 +122,108 @@ __device__ __forceinline__ uint4 scale_row(const uint8_t* row, int kb, int kbyte
                       scale_word(row, kb + 8, kbytes), scale_word(row, kb + 12, kbytes));
 }
 
-__device__ __forceinline__ float act_apply(float z, int act) {
-    if (act == NVFP4KV_ACT_NONE) return z;
-    // z * sigmoid(v): v = z (SiLU), or 2 sqrt(2/pi) (z + 0.044715 z^3) (GELU, tanh form)
-    const float v = act == NVFP4KV_ACT_SILU
-                        ? z
-                        : 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);
-    return __fdividef(z, 1.0f + ex2f(-1.4426950408889634f * v));
+// z * sigmoid(v) for two values, v = z (SiLU) or 2 sqrt(2/pi) (z + 0.044715 z^3)
+// (GELU, tanh form: (1 + tanh(v/2)) / 2 = sigmoid(v)).  The two quotients share
+// one reciprocal, 1/a = b / (a b), since the special-function unit is what a
+// tile's activation waits for (1.5 instead of 2 operations a value); -v log2 e
+// is held to 60, so that a b stays finite: sigmoid below 2^-60 is lost to z's
+// last place many times over.
+template <int kAct>
+__device__ __forceinline__ float2 act_pair(float2 z) {
+    if (kAct == NVFP4KV_ACT_NONE) return z;
+    float2 x;
+    if (kAct == NVFP4KV_ACT_SILU) {
+        x = __fmul2_rn(z, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    } else {
+        constexpr float c1 = -1.4426950408889634f * 1.5957691216057308f;
+        constexpr float c3 = c1 * 0.044715f;
+        const float2 z2 = __fmul2_rn(z, z);
+        x = __fmul2_rn(z, __ffma2_rn(z2, make_float2(c3, c3), make_float2(c1, c1)));
+    }
+    const float2 e = make_float2(ex2f(fminf(x.x, 60.0f)), ex2f(fminf(x.y, 60.0f)));
+    const float2 d = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d.x * d.y));
+    return __fmul2_rn(z, __fmul2_rn(make_float2(d.y, d.x), make_float2(r, r)));
+}
+
+template <bool kF32>
+struct OutType {
+    using T = float;
+};
+template <>
+struct OutType<false> {
+    using T = __nv_bfloat16;
+};
+__device__ __forceinline__ float load_out(const float* p) { return *p; }
+__device__ __forceinline__ float load_out(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+constexpr int kChunk = 32;      // tokens an epilogue warp takes at a time
+
+// Tokens m .. m + kChunk - 1 of one channel, accumulators in tensor memory at
+// taddr.  A whole chunk under one gate row (whole = true) runs without a test
+// per token, its residual in flight while the accumulators are read; the rest
+// goes token by token.
+template <bool kF32, int kAct, bool kGrouped>
+__device__ __forceinline__ void epilogue_chunk(const MatmulArgs& a, uint32_t taddr, int m, int m_end,
+                                               int n, bool nv, float alpha, float b, float g,
+                                               bool whole) {
+    using T = typename OutType<kF32>::T;
+    uint32_t v[kChunk];
+    tmem_ld32(taddr, v);
+    T* y = static_cast<T*>(a.Y) + (size_t)m * a.ldy + n;
+    const T* r = static_cast<const T*>(a.residual) + (size_t)m * a.ldr + n;
+    if (whole) {
+        T res[kChunk];
+        if (a.residual) {
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) {
+                res[j] = *r;
+                r += a.ldr;
+            }
+        }
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < kChunk; j += 2) {
+            float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+                                  make_float2(alpha, alpha), make_float2(b, b));
+            z = act_pair<kAct>(z);
+            if (a.residual)
+                z = __ffma2_rn(z, make_float2(g, g),
+                               make_float2(load_out(&res[j]), load_out(&res[j + 1])));
+            else
+                z = __fmul2_rn(z, make_float2(g, g));
+            store_out(y, z.x);
+            y += a.ldy;
+            store_out(y, z.y);
+            y += a.ldy;
+        }
+    } else {
+        tmem_wait_ld();
+        if (nv) {
+#pragma unroll
+            for (int j = 0; j < kChunk; j += 2) {
+                float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+                                      make_float2(alpha, alpha), make_float2(b, b));
+                z = act_pair<kAct>(z);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int mm = m + j + k;
+                    if (mm < m_end) {
+                        float w = k ? z.y : z.x;
+                        if (!kGrouped && a.gate)
+                            g = __ldg(a.gate + (size_t)(mm / a.rows_per_gate) * a.N + n);
+                        w *= g;
+                        if (a.residual) w += load_out(r + (size_t)(j + k) * a.ldr);
+                        store_out(y + (size_t)(j + k) * a.ldy, w);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    }
 }
 
 struct TileAt {
@@ -167,7 +262,7 @@ struct Tiles {
     }
 };
 
-template <int TN, bool kGrouped>
+template <int TN, bool kGrouped, bool kF32>
 __global__ void __launch_bounds__(kThreadsMM, 1)
 matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
               const MatmulArgs a) {
@@ -197,7 +292,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.acc_full[i]), 1);
-            mbar_init(smem_u32(&sh.acc_free[i]), 4);
+            mbar_init(smem_u32(&sh.acc_free[i]), 8);
         }
         mbar_init(smem_u32(&sh.drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -299,52 +394,44 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 else if (t + (int)gridDim.x < total) load(t + gridDim.x, 0);
             }
         }
-    } else if (warp < 8) {
+    } else if (warp < kTmaWarp) {
         // ------------------------------------------------------------ epilogue
+        // warp = lane quarter (warp % 4) of every second chunk of the tokens
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         int i = 0;
         for (int t = blockIdx.x; t < total; t += gridDim.x, ++i) {
             const TileAt at = tiles.at(t);
             const int buf = i & 1;
-            bool got = wait_or_abort_m(smem_u32(&sh.acc_full[buf]), (uint32_t)((i >> 1) & 1), abort,
-                                       a.ctl, 61u, i);
-            if (!__all_sync(0xFFFFFFFFu, got)) break;
-            tc_fence_after();
             const int n = at.n0 + (warp & 3) * 32 + lane;
             const bool nv = n < a.N;
+            const bool warp_nv = at.n0 + (warp & 3) * 32 + 31 < a.N;
             const size_t en = (size_t)at.e * a.N + n;
             const float alpha = __ldg(a.x_scale) * __ldg(a.w_scale + at.e);
             const float b = (a.bias && nv) ? __ldg(a.bias + en) : 0.0f;
             float g = (a.gate && kGrouped && nv) ? __ldg(a.gate + en) : 1.0f;
+            bool got = wait_or_abort_m(smem_u32(&sh.acc_full[buf]), (uint32_t)((i >> 1) & 1), abort,
+                                       a.ctl, 61u, i);
+            if (!__all_sync(0xFFFFFFFFu, got)) break;
+            tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < TN && at.m0 + c < at.m_end; c += 16) {
-                uint32_t v[16];
-                tmem_ld16(tmem + lane_base + (uint32_t)(buf * TN + c), v);
-                tmem_wait_ld();
-                if (nv) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int m = at.m0 + c + j;
-                        if (m < at.m_end) {
-                            float z = act_apply(fmaf(__uint_as_float(v[j]), alpha, b), a.act);
-                            if (!kGrouped && a.gate)
-                                g = __ldg(a.gate + (size_t)(m / a.rows_per_gate) * a.N + n);
-                            if (a.gate) z *= g;
-                            if (a.y_f32) {
-                                if (a.residual)
-                                    z += static_cast<const float*>(a.residual)[(size_t)m * a.ldr + n];
-                                static_cast<float*>(a.Y)[(size_t)m * a.ldy + n] = z;
-                            } else {
-                                if (a.residual)
-                                    z += __bfloat162float(static_cast<const __nv_bfloat16*>(
-                                        a.residual)[(size_t)m * a.ldr + n]);
-                                static_cast<__nv_bfloat16*>(a.Y)[(size_t)m * a.ldy + n] =
-                                    __float2bfloat16_rn(z);
-                            }
-                        }
-                    }
+            for (int c = (warp >> 2) % 2 * kChunk; c < TN && at.m0 + c < at.m_end; c += 2 * kChunk) {
+                const int m = at.m0 + c;
+                bool whole = warp_nv && m + kChunk <= at.m_end;
+                if (!kGrouped && a.gate && whole) {
+                    const int row = m / a.rows_per_gate;
+                    whole = (m + kChunk - 1) / a.rows_per_gate == row;
+                    g = __ldg(a.gate + (size_t)row * a.N + n);
                 }
-                __syncwarp();
+                const uint32_t ta = tmem + lane_base + (uint32_t)(buf * TN + c);
+                if (a.act == NVFP4KV_ACT_GELU_TANH)
+                    epilogue_chunk<kF32, NVFP4KV_ACT_GELU_TANH, kGrouped>(a, ta, m, at.m_end, n, nv,
+                                                                          alpha, b, g, whole);
+                else if (a.act == NVFP4KV_ACT_SILU)
+                    epilogue_chunk<kF32, NVFP4KV_ACT_SILU, kGrouped>(a, ta, m, at.m_end, n, nv, alpha,
+                                                                     b, g, whole);
+                else
+                    epilogue_chunk<kF32, NVFP4KV_ACT_NONE, kGrouped>(a, ta, m, at.m_end, n, nv, alpha,
+                                                                     b, g, whole);
             }
             tc_fence_before();
             __syncwarp();
@@ -483,7 +570,7 @@ int sm_count_of(int dev) {
     return n;
 }
 
-template <int TN, bool kGrouped>
+template <int TN, bool kGrouped, bool kF32>
 nvfp4kv_status launch_tn(const MatmulArgs& a, const void* w_codes, const void* x_codes,
                          cudaStream_t stream) {
     CUtensorMap map_w, map_x;
@@ -492,7 +579,7 @@ nvfp4kv_status launch_tn(const MatmulArgs& a, const void* w_codes, const void* x
         return NVFP4KV_ERR_CUDA;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4KV_ERR_CUDA;
-    if (cudaFuncSetAttribute(matmul_kernel<TN, kGrouped>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(matmul_kernel<TN, kGrouped, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)Shape<TN>::kSmem) != cudaSuccess)
         return NVFP4KV_ERR_CUDA;
     const long long n_tiles = (a.N + kTileN - 1) / kTileN;
@@ -501,25 +588,28 @@ nvfp4kv_status launch_tn(const MatmulArgs& a, const void* w_codes, const void* x
     const int sms = sm_count_of(dev);
     const int grid = (int)(most < sms ? most : sms);
     if (grid <= 0) return NVFP4KV_ERR_CUDA;
-    matmul_kernel<TN, kGrouped><<<grid, kThreadsMM, Shape<TN>::kSmem, stream>>>(map_w, map_x, a);
+    matmul_kernel<TN, kGrouped, kF32><<<grid, kThreadsMM, Shape<TN>::kSmem, stream>>>(map_w, map_x, a);
     return cudaGetLastError() == cudaSuccess ? NVFP4KV_OK : NVFP4KV_ERR_CUDA;
 }
 
-template <bool kGrouped>
+template <bool kGrouped, bool kF32>
 nvfp4kv_status launch_any(const MatmulArgs& a, const void* w_codes, const void* x_codes,
                           cudaStream_t stream) {
     const int per = kGrouped ? (a.M + a.E - 1) / a.E : a.M;
-    if (per <= 32) return launch_tn<32, kGrouped>(a, w_codes, x_codes, stream);
-    if (per <= 128) return launch_tn<128, kGrouped>(a, w_codes, x_codes, stream);
-    return launch_tn<192, kGrouped>(a, w_codes, x_codes, stream);
+    if (per <= 32) return launch_tn<32, kGrouped, kF32>(a, w_codes, x_codes, stream);
+    if (per <= 128) return launch_tn<128, kGrouped, kF32>(a, w_codes, x_codes, stream);
+    return launch_tn<192, kGrouped, kF32>(a, w_codes, x_codes, stream);
 }
 
 }  // namespace
 
 nvfp4kv_status launch_matmul(const MatmulArgs& a, const void* w_codes, const void* x_codes,
                              cudaStream_t stream) {
-    return a.offsets ? launch_any<true>(a, w_codes, x_codes, stream)
-                     : launch_any<false>(a, w_codes, x_codes, stream);
+    if (a.offsets)
+        return a.y_f32 ? launch_any<true, true>(a, w_codes, x_codes, stream)
+                       : launch_any<true, false>(a, w_codes, x_codes, stream);
+    return a.y_f32 ? launch_any<false, true>(a, w_codes, x_codes, stream)
+                   : launch_any<false, false>(a, w_codes, x_codes, stream);
 }
 
 }  // namespace nvfp4kv

@@ -8,6 +8,7 @@ loudly when the compiled library is missing; there is no fallback path.
 The names mirror the C ABI in include/nvfp4kv.h.
 """
 import ctypes
+import functools
 import math
 import os
 
@@ -140,6 +141,13 @@ def load():
     return L
 
 
+@functools.cache
+def _torch():
+    """torch, imported at the first call that needs it."""
+    import torch
+    return torch
+
+
 def _check(status, where):
     if status != OK:
         raise NvFp4KvError(status, where)
@@ -260,7 +268,7 @@ BLOCKS_1D, TILES_2D = 1, 2
 
 
 def _check_part(t, shape, dtype, name):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} {shape} tensor, "
                          f"got {t.dtype} {tuple(t.shape)}")
 
@@ -336,55 +344,61 @@ ACT_NONE, ACT_GELU_TANH, ACT_SILU = 0, 1, 2      # nvfp4kv_activation
 
 
 def _matrix_view(X):
-    return MatrixView(_ptr(X.codes), _ptr(X.scales), _ptr(X.tensor_scale), X.mode)
+    return MatrixView(X.codes.data_ptr(), X.scales.data_ptr(), X.tensor_scale.data_ptr(), X.mode)
 
 
-def _rows(t, name, M, N, dtype=None):
+def _row_stride(t, name, M, N):
     """Row stride of a [M, N] tensor whose rows are contiguous."""
-    if t.dim() != 2 or tuple(t.shape) != (M, N) or (N > 1 and t.stride(1) != 1) or \
-            (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be a {dtype or ''} [{M}, {N}] tensor with contiguous "
-                         f"rows, got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
-    return t.stride(0) if M > 1 else max(N, t.stride(0))
+    if t.shape != (M, N) or (N > 1 and t.stride(1) != 1) or (M > 1 and t.stride(0) < N):
+        raise ValueError(f"{name} must be a [{M}, {N}] tensor with contiguous rows, "
+                         f"got {tuple(t.shape)} strides {t.stride()}")
+    return t.stride(0) if M > 1 else N
 
 
-def _matmul_args(X, W, Y, bias, activation, gate, gate_rows, rows_per_gate, residual, lead, extra):
-    """Checks shared by the products; the epilogue and Y's row stride."""
-    import torch
+def _matmul_args(X, W, Y, ws, bias, activation, gate, gate_rows, rows_per_gate, residual, lead):
+    """Checks that the products share; the epilogue and Y's row stride."""
     M, N = X.M, W.M
     if X.N != W.N:
         raise ValueError(f"X has {X.N} columns and W {W.N}")
-    _dtype_code(Y)
-    ldy = _rows(Y, "Y", M, N)
     ep = Epilogue(None, activation, None, rows_per_gate, None, 0)
+    operands = [X.codes, W.codes, ws]
     if bias is not None:
-        _check_part(bias, lead + (N,), torch.float32, "bias")
-        ep.bias = _ptr(bias)
+        _check_part(bias, lead + (N,), _torch().float32, "bias")
+        ep.bias = bias.data_ptr()
+        operands.append(bias)
     if gate is not None:
-        _check_part(gate, (gate_rows, N), torch.float32, "gate")
-        ep.gate = _ptr(gate)
+        _check_part(gate, (gate_rows, N), _torch().float32, "gate")
+        ep.gate = gate.data_ptr()
+        operands.append(gate)
     if residual is not None:
-        ep.ld_residual = _rows(residual, "residual", M, N, Y.dtype)
-        ep.residual = _ptr(residual)
-    for t in (X.codes, X.scales, X.tensor_scale, W.codes, W.scales, W.tensor_scale, bias, gate,
-              residual) + extra:
-        if t is not None and t.device != Y.device:
+        if residual.dtype != Y.dtype:
+            raise TypeError(f"residual is {residual.dtype}, Y {Y.dtype}")
+        ep.ld_residual = _row_stride(residual, "residual", M, N)
+        ep.residual = residual.data_ptr()
+        operands.append(residual)
+    device = Y.get_device()
+    for t in operands:
+        if t.get_device() != device:
             raise ValueError(f"operands on {t.device} and {Y.device}")
-    return ep, ldy
+    return ep, _row_stride(Y, "Y", M, N)
 
 
 def _on_device_of(Y, stream, call):
     """call(stream handle) with Y's device current; stream None is that
     device's current stream."""
-    import torch
-    if Y.device.type != "cuda":
+    torch, device = _torch(), Y.get_device()
+    if device < 0:
         raise ValueError(f"Y is on {Y.device}")
     if stream is None:
-        stream = torch.cuda.current_stream(Y.device)
-    if torch.cuda.current_device() == Y.device.index:
-        return call(_stream(stream))
-    with torch.cuda.device(Y.device):
-        return call(_stream(stream))
+        # current_stream(device).cuda_stream without the Stream object, whose
+        # making takes half as long as the launch
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        stream = _stream(stream)
+    if torch.cuda.current_device() == device:
+        return call(stream)
+    with torch.cuda.device(device):
+        return call(stream)
 
 
 def matmul(X: "MatrixBuffer", W: "MatrixBuffer", Y, ws, bias=None, activation=ACT_NONE, gate=None,
@@ -396,12 +410,11 @@ def matmul(X: "MatrixBuffer", W: "MatrixBuffer", Y, ws, bias=None, activation=AC
     if gate is not None and rows_per_gate < 1:
         raise ValueError(f"rows_per_gate {rows_per_gate} with a gate")
     gate_rows = -(-X.M // rows_per_gate) if gate is not None else 0
-    ep, ldy = _matmul_args(X, W, Y, bias, activation, gate, gate_rows, rows_per_gate, residual,
-                           (), (ws,))
+    ep, ldy = _matmul_args(X, W, Y, ws, bias, activation, gate, gate_rows, rows_per_gate,
+                           residual, ())
     xv, wv = _matrix_view(X), _matrix_view(W)
     _check(_on_device_of(Y, stream, lambda s: load().nvfp4kv_matmul(
-        ctypes.byref(xv), ctypes.byref(wv), X.M, W.M, X.N, ctypes.byref(ep), _ptr(Y), ldy,
-        _dtype_code(Y), _ptr(ws), s)), "nvfp4kv_matmul")
+        xv, wv, X.M, W.M, X.N, ep, Y.data_ptr(), ldy, _dtype_code(Y), ws.data_ptr(), s)), "nvfp4kv_matmul")
 
 
 def grouped_matmul(X: "MatrixBuffer", W: "GroupedMatrixBuffer", offsets, Y, ws, bias=None,
@@ -409,14 +422,14 @@ def grouped_matmul(X: "MatrixBuffer", W: "GroupedMatrixBuffer", offsets, Y, ws, 
     """matmul by groups of rows: rows offsets[e] .. offsets[e + 1] - 1 of X
     times matrix e of W; rows outside the groups of Y are left as they are.
     offsets: int32 [E + 1] on the device; bias and gate [E, N] float32."""
-    import torch
-    _check_part(offsets, (W.E + 1,), torch.int32, "offsets")
-    ep, ldy = _matmul_args(X, W, Y, bias, activation, gate, W.E, 0, residual, (W.E,),
-                           (ws, offsets))
+    _check_part(offsets, (W.E + 1,), _torch().int32, "offsets")
+    if offsets.device != Y.device:
+        raise ValueError(f"operands on {offsets.device} and {Y.device}")
+    ep, ldy = _matmul_args(X, W, Y, ws, bias, activation, gate, W.E, 0, residual, (W.E,))
     xv, wv = _matrix_view(X), _matrix_view(W)
     _check(_on_device_of(Y, stream, lambda s: load().nvfp4kv_grouped_matmul(
-        ctypes.byref(xv), ctypes.byref(wv), W.E, X.M, W.M, X.N, _ptr(offsets), ctypes.byref(ep),
-        _ptr(Y), ldy, _dtype_code(Y), _ptr(ws), s)), "nvfp4kv_grouped_matmul")
+        xv, wv, W.E, X.M, W.M, X.N, offsets.data_ptr(), ep, Y.data_ptr(), ldy, _dtype_code(Y),
+        ws.data_ptr(), s)), "nvfp4kv_grouped_matmul")
 
 
 def attention_launches(n_chunks, T_c, H, T_q, d=HEAD_DIM) -> int:

@@ -25,6 +25,8 @@
 // (32x128b.warpx4) places in 4 columns of every lane quarter.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_ptx.cuh"
@@ -564,10 +566,28 @@ bool make_map(CUtensorMap* map, const void* codes, int K, int rows, int depth, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int kMaxDevices = 64;
+
+// Multiprocessors of a device, asked for once (0: no answer).
 int sm_count_of(int dev) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    static std::atomic<int> known[kMaxDevices];
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+        known[dev].store(n, std::memory_order_relaxed);
     return n;
+}
+
+// Allow the kernel its shared memory, once on each device.
+template <int TN, bool kGrouped, bool kF32>
+bool configure(int dev) {
+    static std::atomic<bool> done[kMaxDevices];
+    if (done[dev].load(std::memory_order_relaxed)) return true;
+    if (cudaFuncSetAttribute(matmul_kernel<TN, kGrouped, kF32>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)Shape<TN>::kSmem) != cudaSuccess)
+        return false;
+    done[dev].store(true, std::memory_order_relaxed);
+    return true;
 }
 
 template <int TN, bool kGrouped, bool kF32>
@@ -578,9 +598,8 @@ nvfp4kv_status launch_tn(const MatmulArgs& a, const void* w_codes, const void* x
         !make_map(&map_x, x_codes, a.K, a.M, 1, TN))
         return NVFP4KV_ERR_CUDA;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4KV_ERR_CUDA;
-    if (cudaFuncSetAttribute(matmul_kernel<TN, kGrouped, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)Shape<TN>::kSmem) != cudaSuccess)
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices ||
+        !configure<TN, kGrouped, kF32>(dev))
         return NVFP4KV_ERR_CUDA;
     const long long n_tiles = (a.N + kTileN - 1) / kTileN;
     // grouped: at most one more token tile per expert than the rows fill

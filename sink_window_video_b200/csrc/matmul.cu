@@ -12,11 +12,11 @@
 // row of Y.
 //
 // One persistent CTA per SM over a static tile list; roles by warp:
-//   warps 0-3  block scales: global -> registers (a stage ahead) -> shared
-//              memory in the tensor core's scale layout (below)
-//   warps 4-11 epilogue: tensor memory -> registers -> Y
-//   warp 12    TMA loads of both code tiles (lane 0)
-//   warp 13    tcgen05.cp of the scales into tensor memory and the MMAs (lane 0)
+//   warps 0-3  block scales, a stage each in turn: global -> registers ->
+//              shared memory in the tensor core's scale layout (below)
+//   warp 4     TMA loads of both code tiles (lane 0)
+//   warp 5     tcgen05.cp of the scales into tensor memory and the MMAs (lane 0)
+//   warps 8-15 epilogue: tensor memory -> registers -> Y
 // A stage holds 256 elements along k: 128 bytes of codes a row (one 128-byte
 // swizzle row) and 16 scale bytes a row.  Two accumulators in tensor memory
 // let the epilogue of one tile run under the next tile's MMAs.
@@ -37,8 +37,11 @@ namespace {
 
 constexpr int kTileN = 128;                 // output channels of a tile (the MMA's M)
 constexpr int kStageK = 256;                // elements along k of one stage
-constexpr int kThreadsMM = 448;
-constexpr int kTmaWarp = 12, kMmaWarp = 13;
+constexpr int kThreadsMM = 512;
+constexpr int kScaleWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kEpiWarp0 = 8;   // 6, 7: idle
+// Registers of a thread: 128 at launch (65536 / 512), 80 for the first two
+// warpgroups and 176 for the epilogue's (256 * 80 + 256 * 176 = 65536).
+constexpr int kFewRegs = 80, kManyRegs = 176;
 constexpr int kColsMM = 512;                // tensor-memory columns
 constexpr uint32_t kColSFAm = 448, kColSFBm = 464;   // 16 and 32 columns
 constexpr int kATile = kTileN * 128;        // bytes of codes of a weight tile's stage
@@ -53,6 +56,9 @@ struct Shape {
     static constexpr int kStages = (200 * 1024) / kStage < kMaxStages ? (200 * 1024) / kStage
                                                                       : kMaxStages;
     static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+    // a scale warp waits for the stage's last use by its parity alone, which is
+    // unambiguous only while no warp is more than kStages steps ahead
+    static_assert(kScaleWarps <= kStages, "one phase of a stage at a time");
     static_assert(kStage % 1024 == 0, "stages keep the swizzle alignment");
     static_assert(2 * TN <= (int)kColSFAm, "two accumulators beside the scales");
 };
@@ -93,6 +99,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(mbar)
         : "memory");
+}
+
+template <int R>
+__device__ __forceinline__ void reg_dealloc() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void reg_alloc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
 }
 
 __device__ __forceinline__ void mbar_expect_tx(uint32_t mbar, uint32_t bytes) {
@@ -162,69 +177,84 @@ __device__ __forceinline__ float load_out(const __nv_bfloat16* p) { return __bfl
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-constexpr int kChunk = 32;      // tokens an epilogue warp takes at a time
+// The next row's address.  The empty asm keeps the compiler from forming every
+// multiple of the row stride ahead of the loops (two registers each).
+template <class T>
+__device__ __forceinline__ void next_row(T*& p, long long ld) {
+    p += ld;
+    asm("" : "+l"(p));
+}
 
-// Tokens m .. m + kChunk - 1 of one channel, accumulators in tensor memory at
-// taddr.  A whole chunk under one gate row (whole = true) runs without a test
-// per token, its residual in flight while the accumulators are read; the rest
-// goes token by token.
+constexpr int kChunk = 16;      // tokens an epilogue warp takes at a time
+
+// Tokens m .. m + C - 1 of one channel, accumulators in tensor memory at taddr.
+// kTest: tokens from m_end on and channels from N on are left out, and the gate
+// is looked up for each token; otherwise the C tokens are whole and share the
+// gate g.  The residual's (and gates') loads are all in flight while the
+// accumulators are read.
+template <int C, bool kF32, int kAct, bool kGrouped, bool kTest>
+__device__ __forceinline__ void epilogue_tokens(const MatmulArgs& a, uint32_t taddr, int m, int m_end,
+                                                int n, float alpha, float b, float g) {
+    using T = typename OutType<kF32>::T;
+    const int count = kTest ? (n < a.N ? m_end - m : 0) : C;
+    uint32_t v[C];
+    if (C == 32) tmem_ld32(taddr, v);
+    else tmem_ld16(taddr, v);
+    T* y = static_cast<T*>(a.Y) + (size_t)m * a.ldy + n;
+    T res[C];
+    if (a.residual) {
+        const T* r = static_cast<const T*>(a.residual) + (size_t)m * a.ldr + n;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            if (!kTest || j < count) res[j] = *r;
+            next_row(r, a.ldr);
+        }
+    }
+    constexpr bool kGates = kTest && !kGrouped;
+    float gates[kGates ? C : 1];
+    if (kGates && a.gate) {
+        int q = m / a.rows_per_gate, rem = m - q * a.rows_per_gate;
+        const float* gp = a.gate + (size_t)q * a.N + n;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            if (j < count) gates[j] = __ldg(gp);
+            if (++rem == a.rows_per_gate) {
+                rem = 0;
+                next_row(gp, a.N);
+            }
+        }
+    }
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < C; j += 2) {
+        float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+                              make_float2(alpha, alpha), make_float2(b, b));
+        z = act_pair<kAct>(z);
+        float2 gg = make_float2(g, g);
+        if (kGates && a.gate) gg = make_float2(gates[j], gates[j + 1]);
+        if (a.residual)
+            z = __ffma2_rn(z, gg, make_float2(load_out(&res[j]), load_out(&res[j + 1])));
+        else
+            z = __fmul2_rn(z, gg);
+        if (!kTest || j < count) store_out(y, z.x);
+        next_row(y, a.ldy);
+        if (!kTest || j + 1 < count) store_out(y, z.y);
+        next_row(y, a.ldy);
+    }
+}
+
 template <bool kF32, int kAct, bool kGrouped>
 __device__ __forceinline__ void epilogue_chunk(const MatmulArgs& a, uint32_t taddr, int m, int m_end,
-                                               int n, bool nv, float alpha, float b, float g,
-                                               bool whole) {
-    using T = typename OutType<kF32>::T;
-    uint32_t v[kChunk];
-    tmem_ld32(taddr, v);
-    T* y = static_cast<T*>(a.Y) + (size_t)m * a.ldy + n;
-    const T* r = static_cast<const T*>(a.residual) + (size_t)m * a.ldr + n;
+                                               int n, float alpha, float b, float g, bool whole) {
     if (whole) {
-        T res[kChunk];
-        if (a.residual) {
-#pragma unroll
-            for (int j = 0; j < kChunk; ++j) {
-                res[j] = *r;
-                r += a.ldr;
-            }
-        }
-        tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < kChunk; j += 2) {
-            float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
-                                  make_float2(alpha, alpha), make_float2(b, b));
-            z = act_pair<kAct>(z);
-            if (a.residual)
-                z = __ffma2_rn(z, make_float2(g, g),
-                               make_float2(load_out(&res[j]), load_out(&res[j + 1])));
-            else
-                z = __fmul2_rn(z, make_float2(g, g));
-            store_out(y, z.x);
-            y += a.ldy;
-            store_out(y, z.y);
-            y += a.ldy;
-        }
+        epilogue_tokens<kChunk, kF32, kAct, kGrouped, false>(a, taddr, m, m_end, n, alpha, b, g);
     } else {
-        tmem_wait_ld();
-        if (nv) {
-#pragma unroll
-            for (int j = 0; j < kChunk; j += 2) {
-                float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
-                                      make_float2(alpha, alpha), make_float2(b, b));
-                z = act_pair<kAct>(z);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int mm = m + j + k;
-                    if (mm < m_end) {
-                        float w = k ? z.y : z.x;
-                        if (!kGrouped && a.gate)
-                            g = __ldg(a.gate + (size_t)(mm / a.rows_per_gate) * a.N + n);
-                        w *= g;
-                        if (a.residual) w += load_out(r + (size_t)(j + k) * a.ldr);
-                        store_out(y + (size_t)(j + k) * a.ldy, w);
-                    }
-                }
-            }
+#pragma unroll 1
+        for (int c = 0; c < kChunk && m + c < m_end; c += 16) {
+            epilogue_tokens<16, kF32, kAct, kGrouped, true>(a, taddr + c, m + c, m_end, n, alpha, b,
+                                                            g);
+            __syncwarp();
         }
-        __syncwarp();
     }
 }
 
@@ -289,7 +319,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         sh.abort = 0;
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(smem_u32(&sh.tma_full[s]), 1);
-            mbar_init(smem_u32(&sh.sf_full[s]), 4);
+            mbar_init(smem_u32(&sh.sf_full[s]), 1);
             mbar_init(smem_u32(&sh.empty[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -342,61 +372,87 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     const int steps = (a.K + kStageK - 1) / kStageK;
     const int kbytes = a.K / 16;
 
-    if (warp < 4) {
+    if (warp < kEpiWarp0) reg_dealloc<kFewRegs>();
+    else reg_alloc<kManyRegs>();
+    if (warp < kTmaWarp) {
         // ------------------------------------------------------------ block scales
-        // thread = row of each 128-row group: 16 bytes of the weight row and of
-        // TN / 128 token rows per stage, loaded one stage ahead
-        constexpr int kRows = (TN + 127) / 128;
+        // warp w takes every kScaleWarps-th stage: lane l has rows l, 32 + l, ..
+        // of the weight and the token tile, 16 bytes each, loaded while the
+        // warps before it hold the turn; four rows' words of one K = 64 step
+        // are one 16-byte line of the layout
+        constexpr int kXRows = TN / 32;
+        constexpr int kSfbGroups = (TN + 127) / 128;
         const bool withhold = blockIdx.x == 0 && warp == 0 && (a.ctl->test_flags & 1u) != 0u;
-        const uint32_t line = (uint32_t)(lane * 16 + warp * 4);
-        uint4 wv, xv[kRows];
-        TileAt cur;
-        auto load = [&](int t, int s) {
-            if (s == 0) cur = tiles.at(t);
-            const int n = cur.n0 + tid;
-            wv = make_uint4(0u, 0u, 0u, 0u);
-            if (n < a.N)
-                wv = scale_row(a.w_scales + ((size_t)cur.e * a.w_scale_rows + (n >> a.w_shift)) *
-                                                kbytes,
-                               s * 16, kbytes);
+        uint4 wv[4], xv[kXRows];
+        auto load = [&](const TileAt& at, int s) {
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const int r = 128 * i + tid, m = cur.m0 + r;
+            for (int i = 0; i < 4; ++i) {
+                const int n = at.n0 + 32 * i + lane;
+                wv[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (n < a.N)
+                    wv[i] = scale_row(a.w_scales + ((size_t)at.e * a.w_scale_rows +
+                                                    (n >> a.w_shift)) * kbytes,
+                                      s * 16, kbytes);
+            }
+#pragma unroll
+            for (int i = 0; i < kXRows; ++i) {
+                const int m = at.m0 + 32 * i + lane;
                 xv[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < TN && m < cur.m_end)
+                if (m < at.m_end)
                     xv[i] = scale_row(a.x_scales + (size_t)(m >> a.x_shift) * kbytes, s * 16, kbytes);
             }
         };
-        auto put = [&](uint8_t* dst, const uint4& v, int stride) {
-            *reinterpret_cast<uint32_t*>(dst + line) = v.x;
-            *reinterpret_cast<uint32_t*>(dst + line + stride) = v.y;
-            *reinterpret_cast<uint32_t*>(dst + line + 2 * stride) = v.z;
-            *reinterpret_cast<uint32_t*>(dst + line + 3 * stride) = v.w;
+        auto put4 = [&](uint8_t* dst, int stride, const uint4& r0, const uint4& r1, const uint4& r2,
+                        const uint4& r3) {
+            uint4* d = reinterpret_cast<uint4*>(dst + lane * 16);
+            const int q = stride / 16;
+            d[0] = make_uint4(r0.x, r1.x, r2.x, r3.x);
+            d[q] = make_uint4(r0.y, r1.y, r2.y, r3.y);
+            d[2 * q] = make_uint4(r0.z, r1.z, r2.z, r3.z);
+            d[3 * q] = make_uint4(r0.w, r1.w, r2.w, r3.w);
         };
-        int it = 0;
-        bool ok = true;
-        if ((int)blockIdx.x < total) load(blockIdx.x, 0);
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            for (int s = 0; s < steps; ++s, ++it) {
-                const int st = it % S::kStages;
-                if (it >= S::kStages) {
-                    ok = wait_or_abort_m(smem_u32(&sh.empty[st]),
-                                         (uint32_t)((it / S::kStages - 1) & 1), abort, a.ctl, 60u, it);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (!ok) break;
-                }
-                uint8_t* sf = base + (size_t)st * S::kStage + kATile + S::kBTile;
-                put(sf, wv, 512);
-#pragma unroll
-                for (int i = 0; i < kRows; ++i) put(sf + kSfaBytes + 512 * i, xv[i], 512 * kRows);
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0 && !(withhold && it == 0)) mbar_arrive(smem_u32(&sh.sf_full[st]));
-                if (s + 1 < steps) load(t, s + 1);
-                else if (t + (int)gridDim.x < total) load(t + gridDim.x, 0);
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+        // (t, s): tile and stage of step it
+        int t = blockIdx.x, s = warp;
+        auto settle = [&] {
+            while (s >= steps && t < total) {
+                s -= steps;
+                t += gridDim.x;
             }
+        };
+        settle();
+        int t_at = -1;
+        TileAt at;
+        auto fetch = [&] {
+            if (t >= total) return;
+            if (t != t_at) at = tiles.at(t);
+            t_at = t;
+            load(at, s);
+        };
+        fetch();
+        for (int it = warp; t < total; it += kScaleWarps) {
+            const int st = it % S::kStages;
+            if (it >= S::kStages) {
+                bool ok = wait_or_abort_m(smem_u32(&sh.empty[st]),
+                                          (uint32_t)((it / S::kStages - 1) & 1), abort, a.ctl, 60u, it);
+                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            }
+            uint8_t* sf = base + (size_t)st * S::kStage + kATile + S::kBTile;
+            put4(sf, 512, wv[0], wv[1], wv[2], wv[3]);
+#pragma unroll
+            for (int i = 0; i < kSfbGroups; ++i)
+                put4(sf + kSfaBytes + 512 * i, 512 * kSfbGroups, xv[4 * i],
+                     4 * i + 1 < kXRows ? xv[(4 * i + 1) % kXRows] : none,
+                     4 * i + 2 < kXRows ? xv[(4 * i + 2) % kXRows] : none,
+                     4 * i + 3 < kXRows ? xv[(4 * i + 3) % kXRows] : none);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0 && !(withhold && it == 0)) mbar_arrive(smem_u32(&sh.sf_full[st]));
+            s += kScaleWarps;
+            settle();
+            fetch();
         }
-    } else if (warp < kTmaWarp) {
+    } else if (warp >= kEpiWarp0) {
         // ------------------------------------------------------------ epilogue
         // warp = lane quarter (warp % 4) of every second chunk of the tokens
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -426,14 +482,13 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 }
                 const uint32_t ta = tmem + lane_base + (uint32_t)(buf * TN + c);
                 if (a.act == NVFP4KV_ACT_GELU_TANH)
-                    epilogue_chunk<kF32, NVFP4KV_ACT_GELU_TANH, kGrouped>(a, ta, m, at.m_end, n, nv,
-                                                                          alpha, b, g, whole);
+                    epilogue_chunk<kF32, NVFP4KV_ACT_GELU_TANH, kGrouped>(a, ta, m, at.m_end, n, alpha, b, g, whole);
                 else if (a.act == NVFP4KV_ACT_SILU)
-                    epilogue_chunk<kF32, NVFP4KV_ACT_SILU, kGrouped>(a, ta, m, at.m_end, n, nv, alpha,
-                                                                     b, g, whole);
+                    epilogue_chunk<kF32, NVFP4KV_ACT_SILU, kGrouped>(a, ta, m, at.m_end, n, alpha, b, g,
+                                                                          whole);
                 else
-                    epilogue_chunk<kF32, NVFP4KV_ACT_NONE, kGrouped>(a, ta, m, at.m_end, n, nv, alpha,
-                                                                     b, g, whole);
+                    epilogue_chunk<kF32, NVFP4KV_ACT_NONE, kGrouped>(a, ta, m, at.m_end, n, alpha, b, g,
+                                                                          whole);
             }
             tc_fence_before();
             __syncwarp();
@@ -470,7 +525,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             }
         }
         __syncwarp();
-    } else {
+    } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issue
         if (lane == 0) {
             constexpr uint32_t idesc = umma_idesc_fp4(TN);

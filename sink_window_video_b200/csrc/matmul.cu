@@ -101,6 +101,12 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n.reg .pred P;\nelect.sync _|P, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, P;\n}" : "=r"(p));
+    return p != 0;
+}
+
 template <int R>
 __device__ __forceinline__ void reg_dealloc() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
@@ -527,31 +533,34 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         __syncwarp();
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issue
-        if (lane == 0) {
-            constexpr uint32_t idesc = umma_idesc_fp4(TN);
-            constexpr int kSfbGroups = (TN + 127) / 128;
-            int it = 0, i = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++i) {
-                const int buf = i & 1;
-                if (i >= 2) {
-                    ok = wait_or_abort_m(smem_u32(&sh.acc_free[buf]), (uint32_t)((i / 2 - 1) & 1),
-                                         abort, a.ctl, 63u, i);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                const uint32_t d = tmem + (uint32_t)(buf * TN);
-                for (int s = 0; s < steps; ++s, ++it) {
-                    const int st = it % S::kStages;
-                    const uint32_t par = (uint32_t)((it / S::kStages) & 1);
-                    ok = wait_or_abort_m(smem_u32(&sh.sf_full[st]), par, abort, a.ctl, 64u, it) &&
-                         wait_or_abort_m(smem_u32(&sh.tma_full[st]), par, abort, a.ctl, 65u, it);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t sa = smem_u32(base + (size_t)st * S::kStage);
-                    const uint32_t sf = sa + kATile + S::kBTile;
-                    const uint64_t da = umma_desc(sa, 16, 1024);
-                    const uint64_t db = umma_desc(sa + kATile, 16, 1024);
+        // the whole warp walks the steps; one elected lane issues
+        constexpr uint32_t idesc = umma_idesc_fp4(TN);
+        constexpr int kSfbGroups = (TN + 127) / 128;
+        int it = 0, i = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++i) {
+            const int buf = i & 1;
+            if (i >= 2) {
+                ok = wait_or_abort_m(smem_u32(&sh.acc_free[buf]), (uint32_t)((i / 2 - 1) & 1),
+                                     abort, a.ctl, 63u, i);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            const uint32_t d = tmem + (uint32_t)(buf * TN);
+            for (int s = 0; s < steps; ++s, ++it) {
+                const int st = it % S::kStages;
+                const uint32_t par = (uint32_t)((it / S::kStages) & 1);
+                ok = wait_or_abort_m(smem_u32(&sh.sf_full[st]), par, abort, a.ctl, 64u, it) &&
+                     wait_or_abort_m(smem_u32(&sh.tma_full[st]), par, abort, a.ctl, 65u, it);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sa = smem_u32(base + (size_t)st * S::kStage);
+                const uint32_t sf = sa + kATile + S::kBTile;
+                const uint64_t da = umma_desc(sa, 16, 1024);
+                const uint64_t db = umma_desc(sa + kATile, 16, 1024);
+                if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         tmem_cp_scales(tmem + kColSFAm + 4u * j,
@@ -567,12 +576,14 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                         mma_fp4(d, da + 2u * j, db + 2u * j, idesc, (s | j) ? 1u : 0u,
                                 tmem + kColSFAm + 4u * j, tmem + kColSFBm + 8u * j);
                     mma_commit(smem_u32(&sh.empty[st]));
+                    if (s == steps - 1) mma_commit(smem_u32(&sh.acc_full[buf]));
                 }
-                if (ok) mma_commit(smem_u32(&sh.acc_full[buf]));
+                __syncwarp();
             }
-            mma_commit(smem_u32(&sh.drain));
-            mbar_wait(smem_u32(&sh.drain), 0u);
         }
+        if (elect_one()) mma_commit(smem_u32(&sh.drain));
+        __syncwarp();
+        mbar_wait(smem_u32(&sh.drain), 0u);
         __syncwarp();
     }
 

@@ -12,14 +12,16 @@
 // row of Y.
 //
 // One persistent CTA per SM over a static tile list; roles by warp:
-//   warps 0-3  block scales, a stage each in turn: global -> registers ->
-//              shared memory in the tensor core's scale layout (below)
+//   warps 0-3  block scales: global -> registers (a turn ahead) -> shared
+//              memory in the tensor core's scale layout (below)
 //   warp 4     TMA loads of both code tiles (lane 0)
 //   warp 5     tcgen05.cp of the scales into tensor memory and the MMAs (lane 0)
 //   warps 8-15 epilogue: tensor memory -> registers -> Y
 // A stage holds 256 elements along k: 128 bytes of codes a row (one 128-byte
-// swizzle row) and 16 scale bytes a row.  Two accumulators in tensor memory
-// let the epilogue of one tile run under the next tile's MMAs.
+// swizzle row).  The block scales (16 bytes a row and stage) travel apart, 4
+// stages at a turn, so that a row's 64 bytes are read together and the scale
+// warps hand over once for 4 stages.  Two accumulators in tensor memory let the
+// epilogue of one tile run under the next tile's MMAs.
 // Scale layout of one K = 64 step and 128 rows: 512 bytes, row r's four block
 // scales (bytes) at (r % 32) * 16 + (r / 32) * 4, which tcgen05.cp
 // (32x128b.warpx4) places in 4 columns of every lane quarter.
@@ -38,34 +40,45 @@ namespace {
 constexpr int kTileN = 128;                 // output channels of a tile (the MMA's M)
 constexpr int kStageK = 256;                // elements along k of one stage
 constexpr int kThreadsMM = 512;
-constexpr int kScaleWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kEpiWarp0 = 8;   // 6, 7: idle
-// Registers of a thread: 128 at launch (65536 / 512), 80 for the first two
-// warpgroups and 176 for the epilogue's (256 * 80 + 256 * 176 = 65536).
-constexpr int kFewRegs = 80, kManyRegs = 176;
+constexpr int kScaleWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kEpiWarp0 = 8, kEpiWarps = 8;   // 6, 7: idle
 constexpr int kColsMM = 512;                // tensor-memory columns
-constexpr uint32_t kColSFAm = 448, kColSFBm = 464;   // 16 and 32 columns
 constexpr int kATile = kTileN * 128;        // bytes of codes of a weight tile's stage
-constexpr int kSfaBytes = 4 * 512;
+// Scales travel in turns of 4 steps; a K = 64 block of a 128-row group takes 512
+// bytes, 16 more apart so that a warp's 16-byte lines fall in different banks.
+constexpr int kTurn = 4;
+constexpr int kSfBlock = 512 + 16;
+constexpr int kSfGroup = 4 * kTurn * kSfBlock;
 constexpr int kMaxStages = 12;
+constexpr unsigned long long kLandNs = 10ull * 1000 * 1000;   // 10 ms
+constexpr size_t kStageRoom = 216 * 1024;    // of 227 KB; the rest: offsets, barriers, alignment
 
-template <int TN>
+// TN tokens a tile; G CTAs (one, or a pair) share its MMAs: each has its own
+// 128 output channels, and stages TN / G of the token rows.
+// Instruction descriptor of the block-scaled MMA (kind::mxf4nvf4, E2M1
+// operands, E4M3 scales, fp32 D) for m x n.
+__host__ __device__ constexpr uint32_t umma_idesc_scaled(uint32_t m, uint32_t n) {
+    return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+template <int TN, int G>
 struct Shape {
-    static constexpr int kBTile = TN * 128;
-    static constexpr int kSfbBytes = 4 * 512 * ((TN + 127) / 128);
-    static constexpr int kStage = kATile + kBTile + kSfaBytes + kSfbBytes;
-    static constexpr int kStages = (200 * 1024) / kStage < kMaxStages ? (200 * 1024) / kStage
-                                                                      : kMaxStages;
-    static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
-    // a scale warp waits for the stage's last use by its parity alone, which is
-    // unambiguous only while no warp is more than kStages steps ahead
-    static_assert(kScaleWarps <= kStages, "one phase of a stage at a time");
+    static constexpr int kBTile = TN / G * 128;
+    static constexpr int kStage = kATile + kBTile;
+    static constexpr int kGroups = 1 + (TN + 127) / 128;     // 128-row groups of scales
+    static constexpr int kSfStage = kGroups * kSfGroup;
+    static constexpr int kFit = (int)((kStageRoom - 2 * kSfStage) / kStage);
+    static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+    static constexpr size_t kSmem = (size_t)kStages * kStage + 2 * kSfStage + 1024;
     static_assert(kStage % 1024 == 0, "stages keep the swizzle alignment");
-    static_assert(2 * TN <= (int)kColSFAm, "two accumulators beside the scales");
+    static constexpr uint32_t kColSFA = 2 * TN, kColSFB = 2 * TN + 16;   // 16 and up to 32 columns
+    static_assert(2 * TN + 16 + 8 * 4 <= kColsMM, "two accumulators beside the scales");
+    static_assert(TN / G % 8 == 0, "whole swizzle atoms of token rows");
 };
 
 struct MMShared {
     uint64_t tma_full[kMaxStages];
-    uint64_t sf_full[kMaxStages];
+    uint64_t sf_full[2];
+    uint64_t sf_empty[2];
     uint64_t empty[kMaxStages];
     uint64_t acc_full[2];
     uint64_t acc_free[2];
@@ -75,9 +88,27 @@ struct MMShared {
     int bad_offsets;
 };
 
+// The address of rank 0's copy of a shared-memory object, in the cluster window.
+__device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+
 __device__ __forceinline__ bool wait_or_abort_m(uint32_t mbar, uint32_t parity, volatile int* abort,
                                                 Control* ctl, unsigned site, unsigned step) {
-    if (mbar_try_wait(mbar, parity)) return true;
+    // the clock is read only once a wait is long: reading it takes longer than
+    // most waits last
+#pragma unroll 1
+    for (int i = 0; i < 4096; ++i)
+        if (mbar_try_wait(mbar, parity)) return true;
     const unsigned long long t0 = globaltimer_ns();
     while (true) {
 #pragma unroll 1
@@ -92,13 +123,21 @@ __device__ __forceinline__ bool wait_or_abort_m(uint32_t mbar, uint32_t parity, 
     }
 }
 
+template <int G>
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
                                             int z, uint32_t mbar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(mbar)
-        : "memory");
+    if (G == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(mbar)
+            : "memory");
+    else      // into this CTA, counted by the leader's barrier
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(mbar)
+            : "memory");
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -107,42 +146,79 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-template <int R>
-__device__ __forceinline__ void reg_dealloc() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
-template <int R>
-__device__ __forceinline__ void reg_alloc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-
 __device__ __forceinline__ void mbar_expect_tx(uint32_t mbar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mbar), "r"(bytes)
                  : "memory");
 }
 
 // 512 bytes (32 rows of 16) of shared memory into 4 columns of all four lane
-// quarters.
+// quarters; for a pair each CTA's own shared memory into its own tensor memory.
+template <int G>
 __device__ __forceinline__ void tmem_cp_scales(uint32_t tmem, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc));
+    if (G == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc));
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc));
 }
 
-// Four consecutive block scales of one row from byte kb of it (zeros from
-// byte kbytes on).  kbytes is even (K a multiple of 32).
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int kb, int kbytes) {
-    const int left = kbytes - kb;
-    if (left <= 0) return 0u;
-    if ((kbytes & 3) == 0) return __ldg(reinterpret_cast<const uint32_t*>(row + kb));
-    const uint32_t lo = __ldg(reinterpret_cast<const uint16_t*>(row + kb));
-    const uint32_t hi = left > 2 ? __ldg(reinterpret_cast<const uint16_t*>(row + kb + 2)) : 0u;
+// D (+)= (W scale_W) (X scale_X)^T; for a pair, D's 256 rows and the token rows
+// lie half in each CTA.
+template <int G>
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc,
+                                           uint32_t accumulate, uint32_t sfa, uint32_t sfb) {
+    if (G == 1)
+        mma_fp4(d, da, db, idesc, accumulate, sfa, sfb);
+    else
+        asm volatile(
+            "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%5], [%6], "
+            "p;\n}" ::"r"(d),
+            "l"(da), "l"(db), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb));
+}
+
+// Arrive, when the MMAs and copies issued so far are done, on this barrier: of
+// the issuing CTA, or of every CTA of the tile.
+template <int G>
+__device__ __forceinline__ void commit_own(uint32_t mbar) {
+    if (G == 1)
+        mma_commit(mbar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar)
+            : "memory");
+}
+template <int G>
+__device__ __forceinline__ void commit_all(uint32_t mbar) {
+    if (G == 1)
+        mma_commit(mbar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+            "[%0], %1;" ::"r"(mbar),
+            "h"((uint16_t)3)
+            : "memory");
+}
+
+// Four block scales of a row of which `left` are left (zeros past them), at a
+// 2-byte aligned address; left is even (K a multiple of 32).
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int left) {
+    const uint32_t lo = left > 0 ? __ldg(reinterpret_cast<const uint16_t*>(p)) : 0u;
+    const uint32_t hi = left > 2 ? __ldg(reinterpret_cast<const uint16_t*>(p + 2)) : 0u;
     return lo | (hi << 16);
 }
 
-// The 16 block scales of one stage of one row.
-__device__ __forceinline__ uint4 scale_row(const uint8_t* row, int kb, int kbytes) {
-    if ((kbytes & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(row + kb));
-    return make_uint4(scale_word(row, kb, kbytes), scale_word(row, kb + 4, kbytes),
-                      scale_word(row, kb + 8, kbytes), scale_word(row, kb + 12, kbytes));
+// 16 bytes at p, or zeros.  One predicated load: as a branch around a load, the
+// join of its two sides waits for the data, and a run of such loads goes one by
+// one instead of together.
+__device__ __forceinline__ uint4 load16_if(const uint8_t* p, bool yes) {
+    uint4 v;
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %5, 0;\n"
+        "mov.u32 %0, 0;\nmov.u32 %1, 0;\nmov.u32 %2, 0;\nmov.u32 %3, 0;\n"
+        "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((int)yes));
+    return v;
 }
 
 // z * sigmoid(v) for two values, v = z (SiLU) or 2 sqrt(2/pi) (z + 0.044715 z^3)
@@ -204,8 +280,8 @@ __device__ __forceinline__ void epilogue_tokens(const MatmulArgs& a, uint32_t ta
     using T = typename OutType<kF32>::T;
     const int count = kTest ? (n < a.N ? m_end - m : 0) : C;
     uint32_t v[C];
-    if (C == 32) tmem_ld32(taddr, v);
-    else tmem_ld16(taddr, v);
+    if (C == 16) tmem_ld16(taddr, v);
+    else tmem_ld8(taddr, v);
     T* y = static_cast<T*>(a.Y) + (size_t)m * a.ldy + n;
     T res[C];
     if (a.residual) {
@@ -249,18 +325,24 @@ __device__ __forceinline__ void epilogue_tokens(const MatmulArgs& a, uint32_t ta
     }
 }
 
+// A chunk that is not whole, 8 tokens at a time.
+template <bool kF32, int kAct, bool kGrouped>
+__device__ __forceinline__ void epilogue_ragged(const MatmulArgs& a, uint32_t taddr, int m, int m_end,
+                                             int n, float alpha, float b, float g) {
+#pragma unroll 1
+    for (int c = 0; c < kChunk && m + c < m_end; c += 8) {
+        epilogue_tokens<8, kF32, kAct, kGrouped, true>(a, taddr + c, m + c, m_end, n, alpha, b, g);
+        __syncwarp();
+    }
+}
+
 template <bool kF32, int kAct, bool kGrouped>
 __device__ __forceinline__ void epilogue_chunk(const MatmulArgs& a, uint32_t taddr, int m, int m_end,
                                                int n, float alpha, float b, float g, bool whole) {
     if (whole) {
         epilogue_tokens<kChunk, kF32, kAct, kGrouped, false>(a, taddr, m, m_end, n, alpha, b, g);
     } else {
-#pragma unroll 1
-        for (int c = 0; c < kChunk && m + c < m_end; c += 16) {
-            epilogue_tokens<16, kF32, kAct, kGrouped, true>(a, taddr + c, m + c, m_end, n, alpha, b,
-                                                            g);
-            __syncwarp();
-        }
+        epilogue_ragged<kF32, kAct, kGrouped>(a, taddr, m, m_end, n, alpha, b, g);
     }
 }
 
@@ -268,15 +350,15 @@ struct TileAt {
     int e, n0, m0, m_end;
 };
 
-template <int TN, bool kGrouped>
+template <int TN, int G, bool kGrouped>
 struct Tiles {
     const MatmulArgs& a;
     const int* s_off;
     const int* s_tile;
-    int n_tiles, e;
-    __device__ Tiles(const MatmulArgs& args, const int* off, const int* tile)
-        : a(args), s_off(off), s_tile(tile), e(0) {
-        n_tiles = (a.N + kTileN - 1) / kTileN;
+    int n_tiles, e, rank;
+    __device__ Tiles(const MatmulArgs& args, const int* off, const int* tile, int rank_)
+        : a(args), s_off(off), s_tile(tile), e(0), rank(rank_) {
+        n_tiles = (a.N + kTileN * G - 1) / (kTileN * G);
     }
     __device__ int total() const {
         return kGrouped ? s_tile[a.E] : ((a.M + TN - 1) / TN) * n_tiles;
@@ -293,18 +375,18 @@ struct Tiles {
         }
         const int mt = t / n_tiles;
         r.e = e;
-        r.n0 = (t - mt * n_tiles) * kTileN;
+        r.n0 = ((t - mt * n_tiles) * G + rank) * kTileN;   // this CTA's channels
         r.m0 = row0 + mt * TN;
         r.m_end = min(m_end, r.m0 + TN);
         return r;
     }
 };
 
-template <int TN, bool kGrouped, bool kF32>
+template <int TN, int G, bool kGrouped, bool kF32>
 __global__ void __launch_bounds__(kThreadsMM, 1)
 matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-              const MatmulArgs a) {
-    using S = Shape<TN>;
+              const __grid_constant__ MatmulArgs a) {
+    using S = Shape<TN, G>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ MMShared sh;
     __shared__ int s_off[kGrouped ? kMaxExperts + 1 : 1];
@@ -312,25 +394,36 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort = &sh.abort;
+    // a pair is a cluster of two CTAs; rank 0 leads (issues its MMAs)
+    const int rank = G == 1 ? 0 : (int)(blockIdx.x & 1u);
+    const int first_tile = blockIdx.x / G, stride = gridDim.x / G;
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
 
     if (warp == kMmaWarp) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(&sh.tmem_base)),
-                     "r"(kColsMM));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        if (G == 1) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(&sh.tmem_base)),
+                         "r"(kColsMM));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(&sh.tmem_base)),
+                         "r"(kColsMM));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        }
     }
     if (tid == 0) {
         sh.abort = 0;
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(smem_u32(&sh.tma_full[s]), 1);
-            mbar_init(smem_u32(&sh.sf_full[s]), 1);
             mbar_init(smem_u32(&sh.empty[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.sf_full[i]), kScaleWarps * G);
+            mbar_init(smem_u32(&sh.sf_empty[i]), 1);
             mbar_init(smem_u32(&sh.acc_full[i]), 1);
-            mbar_init(smem_u32(&sh.acc_free[i]), 8);
+            mbar_init(smem_u32(&sh.acc_free[i]), kEpiWarps * G);
         }
         mbar_init(smem_u32(&sh.drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -338,7 +431,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     if (kGrouped && warp == 0) {
         // tile count prefix over the experts; offsets that decrease or leave
         // [0, M] are reported and nothing is computed
-        const int nt = (a.N + kTileN - 1) / kTileN;
+        const int nt = (a.N + kTileN * G - 1) / (kTileN * G);
         int carry = 0;
         bool bad = false;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
@@ -371,99 +464,105 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     }
     tc_fence_before();
     __syncthreads();
+    if (G == 2) cluster_sync();      // both CTAs' barriers are ready
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
-    Tiles<TN, kGrouped> tiles(a, s_off, s_tile);
+    Tiles<TN, G, kGrouped> tiles(a, s_off, s_tile, rank);
     const int total = tiles.total();
     const int steps = (a.K + kStageK - 1) / kStageK;
+    const int turns = (steps + kTurn - 1) / kTurn;
     const int kbytes = a.K / 16;
+    uint8_t* sf_base = base + (size_t)S::kStages * S::kStage;
 
-    if (warp < kEpiWarp0) reg_dealloc<kFewRegs>();
-    else reg_alloc<kManyRegs>();
     if (warp < kTmaWarp) {
         // ------------------------------------------------------------ block scales
-        // warp w takes every kScaleWarps-th stage: lane l has rows l, 32 + l, ..
-        // of the weight and the token tile, 16 bytes each, loaded while the
-        // warps before it hold the turn; four rows' words of one K = 64 step
-        // are one 16-byte line of the layout
-        constexpr int kXRows = TN / 32;
-        constexpr int kSfbGroups = (TN + 127) / 128;
+        // Per turn, 4 steps (64 scale bytes a row) of every 128-row group.  Unit u
+        // of a warp: rows 32 g + r of group u / 4 (0: weights), g = lane % 4,
+        // r = 8 (u % 4) + 2 warp + lane / 16, bytes 16 q .. 16 q + 15 of the
+        // turn's 64, q = lane / 4 % 4: a row's 64 bytes are read together, and
+        // the words stored together are of 4 row groups and 2 rows.
+        constexpr int kUnits = S::kGroups * 4;
         const bool withhold = blockIdx.x == 0 && warp == 0 && (a.ctl->test_flags & 1u) != 0u;
-        uint4 wv[4], xv[kXRows];
-        auto load = [&](const TileAt& at, int s) {
+        const int g = lane & 3, q = (lane >> 2) & 3;
+        const int r = 2 * warp + (lane >> 4);
+        uint4 w[kUnits];
+        const bool wide = kbytes % 16 == 0 && a.x_shift == 0;
+        auto fetch = [&](const TileAt& at, int turn) {
+            const int kb = turn * 64 + q * 16;
+            const int nw = at.n0 + 32 * g + r, mx = at.m0 + 32 * g + r;
+            const uint8_t* wp = a.w_scales + (size_t)at.e * a.w_scale_rows * kbytes + kb;
+            const uint8_t* xp = a.x_scales + kb;
+            if (wide) {
+                const int n_end = kb < kbytes ? a.N : 0;
+                const int m_end = kb < kbytes ? min(at.m_end, at.m0 + TN) : 0;
+                // rows 8 apart; in tiles rows 16 apart have scale rows 1 apart
+                // (n0 is a multiple of 16)
+                const uint8_t* p = wp + (size_t)(nw >> a.w_shift) * kbytes;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = at.n0 + 32 * i + lane;
-                wv[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (n < a.N)
-                    wv[i] = scale_row(a.w_scales + ((size_t)at.e * a.w_scale_rows +
-                                                    (n >> a.w_shift)) * kbytes,
-                                      s * 16, kbytes);
-            }
+                for (int u = 0; u < 4; ++u) {
+                    w[u] = load16_if(p, nw + 8 * u < n_end);
+                    p += a.w_shift ? (u & 1) * kbytes : 8 * kbytes;
+                }
+                p = xp + (size_t)mx * kbytes;
 #pragma unroll
-            for (int i = 0; i < kXRows; ++i) {
-                const int m = at.m0 + 32 * i + lane;
-                xv[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (m < at.m_end)
-                    xv[i] = scale_row(a.x_scales + (size_t)(m >> a.x_shift) * kbytes, s * 16, kbytes);
-            }
-        };
-        auto put4 = [&](uint8_t* dst, int stride, const uint4& r0, const uint4& r1, const uint4& r2,
-                        const uint4& r3) {
-            uint4* d = reinterpret_cast<uint4*>(dst + lane * 16);
-            const int q = stride / 16;
-            d[0] = make_uint4(r0.x, r1.x, r2.x, r3.x);
-            d[q] = make_uint4(r0.y, r1.y, r2.y, r3.y);
-            d[2 * q] = make_uint4(r0.z, r1.z, r2.z, r3.z);
-            d[3 * q] = make_uint4(r0.w, r1.w, r2.w, r3.w);
-        };
-        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-        // (t, s): tile and stage of step it
-        int t = blockIdx.x, s = warp;
-        auto settle = [&] {
-            while (s >= steps && t < total) {
-                s -= steps;
-                t += gridDim.x;
-            }
-        };
-        settle();
-        int t_at = -1;
-        TileAt at;
-        auto fetch = [&] {
-            if (t >= total) return;
-            if (t != t_at) at = tiles.at(t);
-            t_at = t;
-            load(at, s);
-        };
-        fetch();
-        for (int it = warp; t < total; it += kScaleWarps) {
-            const int st = it % S::kStages;
-            if (it >= S::kStages) {
-                bool ok = wait_or_abort_m(smem_u32(&sh.empty[st]),
-                                          (uint32_t)((it / S::kStages - 1) & 1), abort, a.ctl, 60u, it);
-                if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            }
-            uint8_t* sf = base + (size_t)st * S::kStage + kATile + S::kBTile;
-            put4(sf, 512, wv[0], wv[1], wv[2], wv[3]);
+                for (int u = 4; u < kUnits; ++u) {
+                    w[u] = load16_if(p, mx + 8 * (u & 3) + 128 * (u / 4 - 1) < m_end);
+                    p += (u & 3) == 3 ? 104 * kbytes : 8 * kbytes;
+                }
+            } else {
+                const int m_end = min(at.m_end, at.m0 + TN);
 #pragma unroll
-            for (int i = 0; i < kSfbGroups; ++i)
-                put4(sf + kSfaBytes + 512 * i, 512 * kSfbGroups, xv[4 * i],
-                     4 * i + 1 < kXRows ? xv[(4 * i + 1) % kXRows] : none,
-                     4 * i + 2 < kXRows ? xv[(4 * i + 2) % kXRows] : none,
-                     4 * i + 3 < kXRows ? xv[(4 * i + 3) % kXRows] : none);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0 && !(withhold && it == 0)) mbar_arrive(smem_u32(&sh.sf_full[st]));
-            s += kScaleWarps;
-            settle();
-            fetch();
+                for (int u = 0; u < kUnits; ++u) {
+                    const int i = (u < 4 ? nw : mx + 128 * (u / 4 - 1)) + 8 * (u & 3);
+                    const uint8_t* p = (u < 4 ? wp : xp) +
+                                       (size_t)(i >> (u < 4 ? a.w_shift : a.x_shift)) * kbytes;
+                    const int left = i < (u < 4 ? a.N : m_end) ? kbytes - kb : 0;
+                    w[u] = make_uint4(scale_word(p, left), scale_word(p + 4, left - 4),
+                                      scale_word(p + 8, left - 8), scale_word(p + 12, left - 12));
+                }
+            }
+        };
+        auto put = [&](uint8_t* sf) {
+            uint8_t* line = sf + 4 * q * kSfBlock + r * 16 + g * 4;
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                uint8_t* d = line + (u / 4) * kSfGroup + (u & 3) * 128;
+                *reinterpret_cast<uint32_t*>(d) = w[u].x;
+                *reinterpret_cast<uint32_t*>(d + kSfBlock) = w[u].y;
+                *reinterpret_cast<uint32_t*>(d + 2 * kSfBlock) = w[u].z;
+                *reinterpret_cast<uint32_t*>(d + 3 * kSfBlock) = w[u].w;
+            }
+        };
+        int it = 0;
+        bool ok = true;
+        if (first_tile < total) fetch(tiles.at(first_tile), 0);
+        for (int t = first_tile; t < total && ok; t += stride) {
+            const TileAt at = tiles.at(t);
+            for (int turn = 0; turn < turns; ++turn, ++it) {
+                const int st = it & 1;
+                if (it >= 2) {
+                    ok = wait_or_abort_m(smem_u32(&sh.sf_empty[st]), (uint32_t)((it / 2 - 1) & 1),
+                                            abort, a.ctl, 60u, it);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                }
+                put(sf_base + st * S::kSfStage);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0 && !(withhold && it == 0)) {
+                    if (G == 1) mbar_arrive(smem_u32(&sh.sf_full[st]));
+                    else mbar_arrive_cluster(leader_addr(smem_u32(&sh.sf_full[st])));
+                }
+                if (turn + 1 < turns) fetch(at, turn + 1);
+                else if (t + stride < total) fetch(tiles.at(t + stride), 0);
+            }
         }
     } else if (warp >= kEpiWarp0) {
         // ------------------------------------------------------------ epilogue
         // warp = lane quarter (warp % 4) of every second chunk of the tokens
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         int i = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x, ++i) {
+        for (int t = first_tile; t < total; t += stride, ++i) {
             const TileAt at = tiles.at(t);
             const int buf = i & 1;
             const int n = at.n0 + (warp & 3) * 32 + lane;
@@ -478,7 +577,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             if (!__all_sync(0xFFFFFFFFu, got)) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = (warp >> 2) % 2 * kChunk; c < TN && at.m0 + c < at.m_end; c += 2 * kChunk) {
+            for (int c = (warp - kEpiWarp0) / 4 * kChunk; c < TN && at.m0 + c < at.m_end; c += kEpiWarps / 4 * kChunk) {
                 const int m = at.m0 + c;
                 bool whole = warp_nv && m + kChunk <= at.m_end;
                 if (!kGrouped && a.gate && whole) {
@@ -498,14 +597,17 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.acc_free[buf]));
+            if (lane == 0) {
+                if (G == 1) mbar_arrive(smem_u32(&sh.acc_free[buf]));
+                else mbar_arrive_cluster(leader_addr(smem_u32(&sh.acc_free[buf])));
+            }
         }
     } else if (warp == kTmaWarp) {
         // ------------------------------------------------------------ code tiles
         if (lane == 0) {
             int it = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            for (int t = first_tile; t < total && ok; t += stride) {
                 const TileAt at = tiles.at(t);
                 for (int s = 0; s < steps; ++s, ++it) {
                     const int st = it % S::kStages;
@@ -516,29 +618,35 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                         if (!ok) break;
                     }
                     const uint32_t dst = smem_u32(base + (size_t)st * S::kStage);
-                    const uint32_t bar = smem_u32(&sh.tma_full[st]);
-                    mbar_expect_tx(bar, (uint32_t)(kATile + S::kBTile));
-                    tma_load_3d(dst, &map_w, s * 128, at.n0, at.e, bar);
-                    tma_load_3d(dst + kATile, &map_x, s * 128, at.m0, 0, bar);
+                    // the leader's barrier counts both CTAs' bytes
+                    uint32_t bar = smem_u32(&sh.tma_full[st]);
+                    if (rank == 0) mbar_expect_tx(bar, (uint32_t)(G * (kATile + S::kBTile)));
+                    if (G == 2) bar = leader_addr(bar);
+                    tma_load_3d<G>(dst, &map_w, s * 128, at.n0, at.e, bar);
+                    tma_load_3d<G>(dst + kATile, &map_x, s * 128, at.m0 + rank * (TN / G), 0, bar);
                 }
             }
+            if (ok) {
+                // the last uses of the stages are signalled here before the CTA leaves
+                for (int i = it > S::kStages ? it - S::kStages : 0; i < it && ok; ++i)
+                    ok = wait_or_abort_m(smem_u32(&sh.empty[i % S::kStages]),
+                                            (uint32_t)((i / S::kStages) & 1), abort, a.ctl, 66u, i);
+            }
             if (!ok) {
-                // the loads in flight land before the CTA leaves
-                const int first = it > S::kStages ? it - S::kStages : 0;
-                for (int i = first; i < it; ++i)
-                    mbar_wait(smem_u32(&sh.tma_full[i % S::kStages]),
-                              (uint32_t)((i / S::kStages) & 1));
+                // after a wait that gave up: the loads in flight have landed long
+                // before this ends (a pair's are counted in the other CTA)
+                const unsigned long long t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < kLandNs) __nanosleep(1000);
             }
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp && rank == 0) {
         // ------------------------------------------------------------ MMA issue
         // the whole warp walks the steps; one elected lane issues
-        constexpr uint32_t idesc = umma_idesc_fp4(TN);
-        constexpr int kSfbGroups = (TN + 127) / 128;
-        int it = 0, i = 0;
+        constexpr uint32_t idesc = umma_idesc_scaled(G * kTileN, TN);
+        int it = 0, i = 0, turn = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++i) {
+        for (int t = first_tile; t < total && ok; t += stride, ++i) {
             const int buf = i & 1;
             if (i >= 2) {
                 ok = wait_or_abort_m(smem_u32(&sh.acc_free[buf]), (uint32_t)((i / 2 - 1) & 1),
@@ -550,38 +658,48 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             const uint32_t d = tmem + (uint32_t)(buf * TN);
             for (int s = 0; s < steps; ++s, ++it) {
                 const int st = it % S::kStages;
-                const uint32_t par = (uint32_t)((it / S::kStages) & 1);
-                ok = wait_or_abort_m(smem_u32(&sh.sf_full[st]), par, abort, a.ctl, 64u, it) &&
-                     wait_or_abort_m(smem_u32(&sh.tma_full[st]), par, abort, a.ctl, 65u, it);
+                if (s % kTurn == 0) {
+                    ok = wait_or_abort_m(smem_u32(&sh.sf_full[turn & 1]),
+                                            (uint32_t)((turn / 2) & 1), abort, a.ctl, 64u, it);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                }
+                ok = wait_or_abort_m(smem_u32(&sh.tma_full[st]), (uint32_t)((it / S::kStages) & 1),
+                                        abort, a.ctl, 65u, it);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t sa = smem_u32(base + (size_t)st * S::kStage);
-                const uint32_t sf = sa + kATile + S::kBTile;
+                const uint32_t sf = smem_u32(sf_base) + (uint32_t)((turn & 1) * S::kSfStage +
+                                                                   s % kTurn * 4 * kSfBlock);
                 const uint64_t da = umma_desc(sa, 16, 1024);
                 const uint64_t db = umma_desc(sa + kATile, 16, 1024);
+                const bool last = s == steps - 1;
+                const bool turn_ends = last || s % kTurn == kTurn - 1;
                 if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        tmem_cp_scales(tmem + kColSFAm + 4u * j,
-                                       umma_desc_noswizzle(sf + 512 * j, 16, 128));
+                        tmem_cp_scales<G>(tmem + S::kColSFA + 4u * j,
+                                          umma_desc_noswizzle(sf + kSfBlock * j, 16, 128));
 #pragma unroll
-                        for (int q = 0; q < kSfbGroups; ++q)
-                            tmem_cp_scales(tmem + kColSFBm + 8u * j + 4u * q,
-                                           umma_desc_noswizzle(
-                                               sf + kSfaBytes + 512 * (kSfbGroups * j + q), 16, 128));
+                        for (int q = 1; q < S::kGroups; ++q)
+                            tmem_cp_scales<G>(tmem + S::kColSFB + 8u * j + 4u * (q - 1),
+                                              umma_desc_noswizzle(sf + kSfGroup * q + kSfBlock * j, 16,
+                                                                  128));
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        mma_fp4(d, da + 2u * j, db + 2u * j, idesc, (s | j) ? 1u : 0u,
-                                tmem + kColSFAm + 4u * j, tmem + kColSFBm + 8u * j);
-                    mma_commit(smem_u32(&sh.empty[st]));
-                    if (s == steps - 1) mma_commit(smem_u32(&sh.acc_full[buf]));
+                        mma_scaled<G>(d, da + 2u * j, db + 2u * j, idesc, (s | j) ? 1u : 0u,
+                                tmem + S::kColSFA + 4u * j, tmem + S::kColSFB + 8u * j);
+                    commit_all<G>(smem_u32(&sh.empty[st]));
+                    if (turn_ends) commit_all<G>(smem_u32(&sh.sf_empty[turn & 1]));
+                    if (last) commit_all<G>(smem_u32(&sh.acc_full[buf]));
                 }
                 __syncwarp();
+                turn += turn_ends;
             }
         }
-        if (elect_one()) mma_commit(smem_u32(&sh.drain));
+        if (elect_one()) commit_own<G>(smem_u32(&sh.drain));
         __syncwarp();
         mbar_wait(smem_u32(&sh.drain), 0u);
         __syncwarp();
@@ -589,11 +707,16 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
 
     tc_fence_before();
     __syncthreads();
+    if (G == 2) cluster_sync();      // neither CTA leaves while the other may signal it
     if (warp == kMmaWarp) {
         __syncwarp();
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(kColsMM));
+        if (G == 1)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                         "r"(kColsMM));
+        else
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                         "r"(kColsMM));
     }
 }
 
@@ -644,46 +767,56 @@ int sm_count_of(int dev) {
 }
 
 // Allow the kernel its shared memory, once on each device.
-template <int TN, bool kGrouped, bool kF32>
+template <int TN, int G, bool kGrouped, bool kF32>
 bool configure(int dev) {
     static std::atomic<bool> done[kMaxDevices];
     if (done[dev].load(std::memory_order_relaxed)) return true;
-    if (cudaFuncSetAttribute(matmul_kernel<TN, kGrouped, kF32>,
+    if (cudaFuncSetAttribute(matmul_kernel<TN, G, kGrouped, kF32>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)Shape<TN>::kSmem) != cudaSuccess)
+                             (int)Shape<TN, G>::kSmem) != cudaSuccess)
         return false;
     done[dev].store(true, std::memory_order_relaxed);
     return true;
 }
 
-template <int TN, bool kGrouped, bool kF32>
-nvfp4kv_status launch_tn(const MatmulArgs& a, const void* w_codes, const void* x_codes,
-                         cudaStream_t stream) {
+template <int TN, int G, bool kGrouped, bool kF32>
+nvfp4kv_status launch_tn(const MatmulArgs& a, const void* w_codes, const void* x_codes, int dev,
+                         int sms, cudaStream_t stream) {
     CUtensorMap map_w, map_x;
     if (!make_map(&map_w, w_codes, a.K, a.N, kGrouped ? a.E : 1, kTileN) ||
-        !make_map(&map_x, x_codes, a.K, a.M, 1, TN))
+        !make_map(&map_x, x_codes, a.K, a.M, 1, TN / G) || !configure<TN, G, kGrouped, kF32>(dev))
         return NVFP4KV_ERR_CUDA;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices ||
-        !configure<TN, kGrouped, kF32>(dev))
-        return NVFP4KV_ERR_CUDA;
-    const long long n_tiles = (a.N + kTileN - 1) / kTileN;
+    const long long n_tiles = (a.N + kTileN * G - 1) / (kTileN * G);
     // grouped: at most one more token tile per expert than the rows fill
     const long long most = n_tiles * ((a.M + TN - 1) / TN + (kGrouped ? a.E : 0));
-    const int sms = sm_count_of(dev);
-    const int grid = (int)(most < sms ? most : sms);
-    if (grid <= 0) return NVFP4KV_ERR_CUDA;
-    matmul_kernel<TN, kGrouped, kF32><<<grid, kThreadsMM, Shape<TN>::kSmem, stream>>>(map_w, map_x, a);
-    return cudaGetLastError() == cudaSuccess ? NVFP4KV_OK : NVFP4KV_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(G * (unsigned)(most < sms / G ? most : sms / G));
+    cfg.blockDim = dim3(kThreadsMM);
+    cfg.dynamicSmemBytes = Shape<TN, G>::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = G;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = G > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, matmul_kernel<TN, G, kGrouped, kF32>, map_w, map_x, a) ==
+                   cudaSuccess
+               ? NVFP4KV_OK
+               : NVFP4KV_ERR_CUDA;
 }
 
 template <bool kGrouped, bool kF32>
 nvfp4kv_status launch_any(const MatmulArgs& a, const void* w_codes, const void* x_codes,
                           cudaStream_t stream) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return NVFP4KV_ERR_CUDA;
+    const int sms = sm_count_of(dev);
+    if (sms < 2) return NVFP4KV_ERR_CUDA;
     const int per = kGrouped ? (a.M + a.E - 1) / a.E : a.M;
-    if (per <= 32) return launch_tn<32, kGrouped, kF32>(a, w_codes, x_codes, stream);
-    if (per <= 128) return launch_tn<128, kGrouped, kF32>(a, w_codes, x_codes, stream);
-    return launch_tn<192, kGrouped, kF32>(a, w_codes, x_codes, stream);
+    if (per <= 32) return launch_tn<32, 1, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
+    if (per <= 128) return launch_tn<128, 1, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
+    return launch_tn<192, 2, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
 }
 
 }  // namespace

@@ -60,6 +60,19 @@ __host__ __device__ constexpr uint32_t umma_idesc_scaled(uint32_t m, uint32_t n)
     return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
+// Position in a ring of N slots and the parity of its current pass.
+template <int N>
+struct Ring {
+    int at = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) {
+            at = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
 template <int TN, int G>
 struct Shape {
     static constexpr int kBTile = TN / G * 128;
@@ -540,12 +553,10 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             const TileAt at = tiles.at(t);
             for (int turn = 0; turn < turns; ++turn, ++it) {
                 const int st = it & 1;
-                if (it >= 2) {
-                    ok = wait_or_abort_m(smem_u32(&sh.sf_empty[st]), (uint32_t)((it / 2 - 1) & 1),
-                                            abort, a.ctl, 60u, it);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (!ok) break;
-                }
+                ok = wait_or_abort_m(smem_u32(&sh.sf_empty[st]), (uint32_t)(((it >> 1) & 1) ^ 1), abort,
+                                     a.ctl, 60u, it);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
                 put(sf_base + st * S::kSfStage);
                 fence_async_smem();
                 __syncwarp();
@@ -604,33 +615,32 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         }
     } else if (warp == kTmaWarp) {
         // ------------------------------------------------------------ code tiles
-        if (lane == 0) {
+        if (elect_one()) {
+            Ring<S::kStages> ring;
             int it = 0;
             bool ok = true;
+            const uint32_t stage0 = smem_u32(base);
             for (int t = first_tile; t < total && ok; t += stride) {
                 const TileAt at = tiles.at(t);
-                for (int s = 0; s < steps; ++s, ++it) {
-                    const int st = it % S::kStages;
-                    if (it >= S::kStages) {
-                        ok = wait_or_abort_m(smem_u32(&sh.empty[st]),
-                                             (uint32_t)((it / S::kStages - 1) & 1), abort, a.ctl, 62u,
-                                             it);
-                        if (!ok) break;
-                    }
-                    const uint32_t dst = smem_u32(base + (size_t)st * S::kStage);
+                for (int s = 0; s < steps; ++s, ++it, ring.next()) {
+                    // (the first pass over the ring finds the phase before the first done)
+                    ok = wait_or_abort_m(smem_u32(&sh.empty[ring.at]), ring.phase ^ 1u, abort, a.ctl,
+                                         62u, it);
+                    if (!ok) break;
+                    const uint32_t dst = stage0 + (uint32_t)ring.at * S::kStage;
                     // the leader's barrier counts both CTAs' bytes
-                    uint32_t bar = smem_u32(&sh.tma_full[st]);
+                    uint32_t bar = smem_u32(&sh.tma_full[ring.at]);
                     if (rank == 0) mbar_expect_tx(bar, (uint32_t)(G * (kATile + S::kBTile)));
                     if (G == 2) bar = leader_addr(bar);
                     tma_load_3d<G>(dst, &map_w, s * 128, at.n0, at.e, bar);
                     tma_load_3d<G>(dst + kATile, &map_x, s * 128, at.m0 + rank * (TN / G), 0, bar);
                 }
             }
-            if (ok) {
-                // the last uses of the stages are signalled here before the CTA leaves
-                for (int i = it > S::kStages ? it - S::kStages : 0; i < it && ok; ++i)
-                    ok = wait_or_abort_m(smem_u32(&sh.empty[i % S::kStages]),
-                                            (uint32_t)((i / S::kStages) & 1), abort, a.ctl, 66u, i);
+            // the last uses of the stages are signalled here before the CTA leaves
+            for (int i = min(it, S::kStages); i > 0 && ok; --i, ring.next()) {
+                if (it < S::kStages && i == it) ring = Ring<S::kStages>();
+                ok = wait_or_abort_m(smem_u32(&sh.empty[ring.at]),
+                                     it < S::kStages ? 0u : ring.phase ^ 1u, abort, a.ctl, 66u, i);
             }
             if (!ok) {
                 // after a wait that gave up: the loads in flight have landed long
@@ -642,66 +652,61 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         __syncwarp();
     } else if (warp == kMmaWarp && rank == 0) {
         // ------------------------------------------------------------ MMA issue
-        // the whole warp walks the steps; one elected lane issues
-        constexpr uint32_t idesc = umma_idesc_scaled(G * kTileN, TN);
-        int it = 0, i = 0, turn = 0;
-        bool ok = true;
-        for (int t = first_tile; t < total && ok; t += stride, ++i) {
-            const int buf = i & 1;
-            if (i >= 2) {
-                ok = wait_or_abort_m(smem_u32(&sh.acc_free[buf]), (uint32_t)((i / 2 - 1) & 1),
-                                     abort, a.ctl, 63u, i);
-                ok = __all_sync(0xFFFFFFFFu, ok);
+        // One elected lane walks the steps.  (elect.sync, not lane == 0: knowing
+        // the branch to be one thread, the compiler issues the tensor-core
+        // instructions straight from uniform registers.)
+        if (elect_one()) {
+            constexpr uint32_t idesc = umma_idesc_scaled(G * kTileN, TN);
+            Ring<S::kStages> ring;
+            Ring<2> turn, acc;
+            const uint32_t stage0 = smem_u32(base), sf0 = smem_u32(sf_base);
+            bool ok = true;
+            for (int t = first_tile; t < total && ok; t += stride, acc.next()) {
+                // (the first use of an accumulator finds the phase before the first done)
+                ok = wait_or_abort_m(smem_u32(&sh.acc_free[acc.at]), acc.phase ^ 1u, abort, a.ctl, 63u,
+                                     t);
                 if (!ok) break;
                 tc_fence_after();
-            }
-            const uint32_t d = tmem + (uint32_t)(buf * TN);
-            for (int s = 0; s < steps; ++s, ++it) {
-                const int st = it % S::kStages;
-                if (s % kTurn == 0) {
-                    ok = wait_or_abort_m(smem_u32(&sh.sf_full[turn & 1]),
-                                            (uint32_t)((turn / 2) & 1), abort, a.ctl, 64u, it);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
+                const uint32_t d = tmem + (uint32_t)acc.at * TN;
+                for (int s = 0; s < steps; s += kTurn, turn.next()) {
+                    ok = wait_or_abort_m(smem_u32(&sh.sf_full[turn.at]), turn.phase, abort, a.ctl, 64u,
+                                         s);
                     if (!ok) break;
-                }
-                ok = wait_or_abort_m(smem_u32(&sh.tma_full[st]), (uint32_t)((it / S::kStages) & 1),
-                                        abort, a.ctl, 65u, it);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t sa = smem_u32(base + (size_t)st * S::kStage);
-                const uint32_t sf = smem_u32(sf_base) + (uint32_t)((turn & 1) * S::kSfStage +
-                                                                   s % kTurn * 4 * kSfBlock);
-                const uint64_t da = umma_desc(sa, 16, 1024);
-                const uint64_t db = umma_desc(sa + kATile, 16, 1024);
-                const bool last = s == steps - 1;
-                const bool turn_ends = last || s % kTurn == kTurn - 1;
-                if (elect_one()) {
+                    const uint32_t sf = sf0 + (uint32_t)turn.at * S::kSfStage;
+                    const int n = min(kTurn, steps - s);
+#pragma unroll 1
+                    for (int k = 0; k < n; ++k, ring.next()) {
+                        ok = wait_or_abort_m(smem_u32(&sh.tma_full[ring.at]), ring.phase, abort, a.ctl,
+                                             65u, s);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t sa = stage0 + (uint32_t)ring.at * S::kStage;
+                        const uint64_t da = umma_desc(sa, 16, 1024);
+                        const uint64_t db = umma_desc(sa + kATile, 16, 1024);
+                        const uint64_t ds = umma_desc_noswizzle(sf + k * 4 * kSfBlock, 16, 128);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        tmem_cp_scales<G>(tmem + S::kColSFA + 4u * j,
-                                          umma_desc_noswizzle(sf + kSfBlock * j, 16, 128));
+                        for (int j = 0; j < 4; ++j) {
+                            tmem_cp_scales<G>(tmem + S::kColSFA + 4u * j,
+                                              ds + (uint64_t)((kSfBlock * j) >> 4));
 #pragma unroll
-                        for (int q = 1; q < S::kGroups; ++q)
-                            tmem_cp_scales<G>(tmem + S::kColSFB + 8u * j + 4u * (q - 1),
-                                              umma_desc_noswizzle(sf + kSfGroup * q + kSfBlock * j, 16,
-                                                                  128));
+                            for (int q = 1; q < S::kGroups; ++q)
+                                tmem_cp_scales<G>(tmem + S::kColSFB + 8u * j + 4u * (q - 1),
+                                                  ds + (uint64_t)((kSfGroup * q + kSfBlock * j) >> 4));
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_scaled<G>(d, da + 2u * j, db + 2u * j, idesc, (s | k | j) ? 1u : 0u,
+                                          tmem + S::kColSFA + 4u * j, tmem + S::kColSFB + 8u * j);
+                        commit_all<G>(smem_u32(&sh.empty[ring.at]));
                     }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_scaled<G>(d, da + 2u * j, db + 2u * j, idesc, (s | j) ? 1u : 0u,
-                                tmem + S::kColSFA + 4u * j, tmem + S::kColSFB + 8u * j);
-                    commit_all<G>(smem_u32(&sh.empty[st]));
-                    if (turn_ends) commit_all<G>(smem_u32(&sh.sf_empty[turn & 1]));
-                    if (last) commit_all<G>(smem_u32(&sh.acc_full[buf]));
+                    if (!ok) break;
+                    commit_all<G>(smem_u32(&sh.sf_empty[turn.at]));
                 }
-                __syncwarp();
-                turn += turn_ends;
+                if (ok) commit_all<G>(smem_u32(&sh.acc_full[acc.at]));
             }
+            commit_own<G>(smem_u32(&sh.drain));
+            mbar_wait(smem_u32(&sh.drain), 0u);
         }
-        if (elect_one()) commit_own<G>(smem_u32(&sh.drain));
-        __syncwarp();
-        mbar_wait(smem_u32(&sh.drain), 0u);
         __syncwarp();
     }
 

@@ -280,82 +280,125 @@ __device__ __forceinline__ void next_row(T*& p, long long ld) {
     asm("" : "+l"(p));
 }
 
-constexpr int kChunk = 16;      // tokens an epilogue warp takes at a time
+// What an epilogue thread keeps of its tile: its channel n, that channel's
+// constants, and where the next token's result and residual are.
+template <class T>
+struct Channel {
+    int n;
+    float alpha, bias, gate;
+    T* y;
+    const T* r;
+};
 
-// Tokens m .. m + C - 1 of one channel, accumulators in tensor memory at taddr.
-// kTest: tokens from m_end on and channels from N on are left out, and the gate
-// is looked up for each token; otherwise the C tokens are whole and share the
-// gate g.  The residual's (and gates') loads are all in flight while the
-// accumulators are read.
-template <int C, bool kF32, int kAct, bool kGrouped, bool kTest>
-__device__ __forceinline__ void epilogue_tokens(const MatmulArgs& a, uint32_t taddr, int m, int m_end,
-                                                int n, float alpha, float b, float g) {
-    using T = typename OutType<kF32>::T;
-    const int count = kTest ? (n < a.N ? m_end - m : 0) : C;
+// The next C tokens of one channel, accumulators in tensor memory at taddr, all
+// under ch.gate.  The residual's loads are in flight while the accumulators are
+// read.
+template <int C, int kAct, class T>
+__device__ __forceinline__ void epilogue_whole(const MatmulArgs& a, uint32_t taddr, Channel<T>& ch) {
     uint32_t v[C];
-    if (C == 16) tmem_ld16(taddr, v);
-    else tmem_ld8(taddr, v);
-    T* y = static_cast<T*>(a.Y) + (size_t)m * a.ldy + n;
+    tmem_ld16(taddr, v);
     T res[C];
     if (a.residual) {
-        const T* r = static_cast<const T*>(a.residual) + (size_t)m * a.ldr + n;
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-            if (!kTest || j < count) res[j] = *r;
-            next_row(r, a.ldr);
-        }
-    }
-    constexpr bool kGates = kTest && !kGrouped;
-    float gates[kGates ? C : 1];
-    if (kGates && a.gate) {
-        int q = m / a.rows_per_gate, rem = m - q * a.rows_per_gate;
-        const float* gp = a.gate + (size_t)q * a.N + n;
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            if (j < count) gates[j] = __ldg(gp);
-            if (++rem == a.rows_per_gate) {
-                rem = 0;
-                next_row(gp, a.N);
-            }
+            res[j] = *ch.r;
+            next_row(ch.r, a.ldr);
         }
     }
     tmem_wait_ld();
 #pragma unroll
     for (int j = 0; j < C; j += 2) {
         float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
-                              make_float2(alpha, alpha), make_float2(b, b));
+                              make_float2(ch.alpha, ch.alpha), make_float2(ch.bias, ch.bias));
         z = act_pair<kAct>(z);
-        float2 gg = make_float2(g, g);
-        if (kGates && a.gate) gg = make_float2(gates[j], gates[j + 1]);
         if (a.residual)
-            z = __ffma2_rn(z, gg, make_float2(load_out(&res[j]), load_out(&res[j + 1])));
+            z = __ffma2_rn(z, make_float2(ch.gate, ch.gate),
+                           make_float2(load_out(&res[j]), load_out(&res[j + 1])));
         else
-            z = __fmul2_rn(z, gg);
-        if (!kTest || j < count) store_out(y, z.x);
-        next_row(y, a.ldy);
-        if (!kTest || j + 1 < count) store_out(y, z.y);
-        next_row(y, a.ldy);
+            z = __fmul2_rn(z, make_float2(ch.gate, ch.gate));
+        store_out(ch.y, z.x);
+        next_row(ch.y, a.ldy);
+        store_out(ch.y, z.y);
+        next_row(ch.y, a.ldy);
     }
 }
 
-// A chunk that is not whole, 8 tokens at a time.
-template <bool kF32, int kAct, bool kGrouped>
-__device__ __forceinline__ void epilogue_ragged(const MatmulArgs& a, uint32_t taddr, int m, int m_end,
-                                             int n, float alpha, float b, float g) {
+// The next `count` (at most 8) tokens from row m on; none where the channel is
+// not stored.  gates: each token's gate is looked up.
+template <int kAct, class T>
+__device__ __forceinline__ void epilogue_ragged(const MatmulArgs& a, uint32_t taddr, Channel<T>& ch,
+                                                int m, int count, bool stored, bool gates) {
+    constexpr int C = 8;
+    uint32_t v[C];
+    tmem_ld8(taddr, v);
+    T res[C];
+    float g[C];
+    int q = 0, rem = 0;
+    if (gates) {
+        q = m / a.rows_per_gate;
+        rem = m - q * a.rows_per_gate;
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        const bool here = stored && j < count;
+        g[j] = ch.gate;
+        if (gates) {
+            if (here) g[j] = __ldg(a.gate + (size_t)q * a.N + ch.n);
+            if (++rem == a.rows_per_gate) {
+                rem = 0;
+                ++q;
+            }
+        }
+        if (a.residual) {
+            if (here) res[j] = *ch.r;
+            if (j < count) next_row(ch.r, a.ldr);
+        }
+    }
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < C; j += 2) {
+        float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+                              make_float2(ch.alpha, ch.alpha), make_float2(ch.bias, ch.bias));
+        z = act_pair<kAct>(z);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const bool here = stored && j + k < count;
+            float w = (k ? z.y : z.x) * g[j + k];
+            if (here && a.residual) w = fmaf(k ? z.y : z.x, g[j + k], load_out(&res[j + k]));
+            if (here) store_out(ch.y, w);
+            if (j + k < count) next_row(ch.y, a.ldy);
+        }
+    }
+    __syncwarp();
+}
+
+// One warp's share of a tile: `count` tokens from row m on of 32 channels, their
+// sums in tensor memory from taddr on.
+template <int kAct, bool kGrouped, class T>
+__device__ __forceinline__ void epilogue_share(const MatmulArgs& a, uint32_t taddr, int m, int count,
+                                               Channel<T> ch) {
+    const bool stored = ch.n < a.N;
+    const bool all_stored = __all_sync(0xFFFFFFFFu, stored);
+    // a stretch of tokens under one gate; with fewer than 16 rows a gate, the
+    // gate is looked up token by token
+    const bool by_row = !kGrouped && a.gate;
+    const bool gates = by_row && a.rows_per_gate < 16;
+    int c = 0;
+    while (c < count) {
+        int end = count;
+        if (by_row && !gates) {
+            const int row = (m + c) / a.rows_per_gate;
+            end = (int)min((long long)count, (long long)(row + 1) * a.rows_per_gate - m);
+            ch.gate = stored ? __ldg(a.gate + (size_t)row * a.N + ch.n) : 0.0f;
+        }
+        if (all_stored && !gates) {
 #pragma unroll 1
-    for (int c = 0; c < kChunk && m + c < m_end; c += 8) {
-        epilogue_tokens<8, kF32, kAct, kGrouped, true>(a, taddr + c, m + c, m_end, n, alpha, b, g);
-        __syncwarp();
-    }
-}
-
-template <bool kF32, int kAct, bool kGrouped>
-__device__ __forceinline__ void epilogue_chunk(const MatmulArgs& a, uint32_t taddr, int m, int m_end,
-                                               int n, float alpha, float b, float g, bool whole) {
-    if (whole) {
-        epilogue_tokens<kChunk, kF32, kAct, kGrouped, false>(a, taddr, m, m_end, n, alpha, b, g);
-    } else {
-        epilogue_ragged<kF32, kAct, kGrouped>(a, taddr, m, m_end, n, alpha, b, g);
+            for (; c + 16 <= end; c += 16) epilogue_whole<16, kAct>(a, taddr + c, ch);
+        }
+#pragma unroll 1
+        for (; c < end; c += 8)
+            epilogue_ragged<kAct>(a, taddr + c, ch, m + c, min(8, end - c), stored, gates);
+        c = end;
     }
 }
 
@@ -570,42 +613,37 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         }
     } else if (warp >= kEpiWarp0) {
         // ------------------------------------------------------------ epilogue
-        // warp = lane quarter (warp % 4) of every second chunk of the tokens
+        // warp = lane quarter (warp % 4) of one part of the tile's tokens
+        using T = typename OutType<kF32>::T;
+        constexpr int kPart = TN / (kEpiWarps / 4);
+        const int first = (warp - kEpiWarp0) / 4 * kPart;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         int i = 0;
         for (int t = first_tile; t < total; t += stride, ++i) {
             const TileAt at = tiles.at(t);
             const int buf = i & 1;
-            const int n = at.n0 + (warp & 3) * 32 + lane;
-            const bool nv = n < a.N;
-            const bool warp_nv = at.n0 + (warp & 3) * 32 + 31 < a.N;
-            const size_t en = (size_t)at.e * a.N + n;
-            const float alpha = __ldg(a.x_scale) * __ldg(a.w_scale + at.e);
-            const float b = (a.bias && nv) ? __ldg(a.bias + en) : 0.0f;
-            float g = (a.gate && kGrouped && nv) ? __ldg(a.gate + en) : 1.0f;
-            bool got = wait_or_abort_m(smem_u32(&sh.acc_full[buf]), (uint32_t)((i >> 1) & 1), abort,
-                                       a.ctl, 61u, i);
+            const int m = at.m0 + first;
+            const int count = min(kPart, at.m_end - m);
+            Channel<T> ch;
+            ch.n = at.n0 + (warp & 3) * 32 + lane;
+            const bool nv = ch.n < a.N;
+            const size_t en = (size_t)at.e * a.N + ch.n;
+            ch.alpha = __ldg(a.x_scale) * __ldg(a.w_scale + at.e);
+            ch.bias = (a.bias && nv) ? __ldg(a.bias + en) : 0.0f;
+            ch.gate = (a.gate && kGrouped && nv) ? __ldg(a.gate + en) : 1.0f;
+            ch.y = static_cast<T*>(a.Y) + (size_t)m * a.ldy + ch.n;
+            ch.r = static_cast<const T*>(a.residual) + (size_t)m * a.ldr + ch.n;
+            const bool got = wait_or_abort_m(smem_u32(&sh.acc_full[buf]), (uint32_t)((i >> 1) & 1),
+                                             abort, a.ctl, 61u, i);
             if (!__all_sync(0xFFFFFFFFu, got)) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int c = (warp - kEpiWarp0) / 4 * kChunk; c < TN && at.m0 + c < at.m_end; c += kEpiWarps / 4 * kChunk) {
-                const int m = at.m0 + c;
-                bool whole = warp_nv && m + kChunk <= at.m_end;
-                if (!kGrouped && a.gate && whole) {
-                    const int row = m / a.rows_per_gate;
-                    whole = (m + kChunk - 1) / a.rows_per_gate == row;
-                    g = __ldg(a.gate + (size_t)row * a.N + n);
-                }
-                const uint32_t ta = tmem + lane_base + (uint32_t)(buf * TN + c);
-                if (a.act == NVFP4KV_ACT_GELU_TANH)
-                    epilogue_chunk<kF32, NVFP4KV_ACT_GELU_TANH, kGrouped>(a, ta, m, at.m_end, n, alpha, b, g, whole);
-                else if (a.act == NVFP4KV_ACT_SILU)
-                    epilogue_chunk<kF32, NVFP4KV_ACT_SILU, kGrouped>(a, ta, m, at.m_end, n, alpha, b, g,
-                                                                          whole);
-                else
-                    epilogue_chunk<kF32, NVFP4KV_ACT_NONE, kGrouped>(a, ta, m, at.m_end, n, alpha, b, g,
-                                                                          whole);
-            }
+            const uint32_t ta = tmem + lane_base + (uint32_t)(buf * TN + first);
+            if (a.act == NVFP4KV_ACT_GELU_TANH)
+                epilogue_share<NVFP4KV_ACT_GELU_TANH, kGrouped>(a, ta, m, count, ch);
+            else if (a.act == NVFP4KV_ACT_SILU)
+                epilogue_share<NVFP4KV_ACT_SILU, kGrouped>(a, ta, m, count, ch);
+            else
+                epilogue_share<NVFP4KV_ACT_NONE, kGrouped>(a, ta, m, count, ch);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {

@@ -48,6 +48,10 @@ constexpr int kATile = kTileN * 128;        // bytes of codes of a weight tile's
 constexpr int kTurn = 4;
 constexpr int kSfBlock = 512 + 16;
 constexpr int kSfGroup = 4 * kTurn * kSfBlock;
+constexpr int kChunk = 16;              // tokens an epilogue warp takes at a time
+constexpr int kEpiRow = 36;             // floats from one token's 32 channels to the next's:
+                                        // 16-byte reads of two rows fall in different banks
+constexpr int kEpiBytes = kChunk * kEpiRow * 4;
 constexpr int kMaxStages = 12;
 constexpr unsigned long long kLandNs = 10ull * 1000 * 1000;   // 10 ms
 constexpr size_t kStageRoom = 216 * 1024;    // of 227 KB; the rest: offsets, barriers, alignment
@@ -79,9 +83,9 @@ struct Shape {
     static constexpr int kStage = kATile + kBTile;
     static constexpr int kGroups = 1 + (TN + 127) / 128;     // 128-row groups of scales
     static constexpr int kSfStage = kGroups * kSfGroup;
-    static constexpr int kFit = (int)((kStageRoom - 2 * kSfStage) / kStage);
+    static constexpr int kFit = (int)((kStageRoom - 2 * kSfStage - kEpiWarps * kEpiBytes) / kStage);
     static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
-    static constexpr size_t kSmem = (size_t)kStages * kStage + 2 * kSfStage + 1024;
+    static constexpr size_t kSmem = (size_t)kStages * kStage + 2 * kSfStage + kEpiWarps * kEpiBytes + 1024;
     static_assert(kStage % 1024 == 0, "stages keep the swizzle alignment");
     static constexpr uint32_t kColSFA = 2 * TN, kColSFB = 2 * TN + 16;   // 16 and up to 32 columns
     static_assert(2 * TN + 16 + 8 * 4 <= kColsMM, "two accumulators beside the scales");
@@ -259,146 +263,165 @@ __device__ __forceinline__ float2 act_pair(float2 z) {
     return __fmul2_rn(z, __fmul2_rn(make_float2(d.y, d.x), make_float2(r, r)));
 }
 
+// A 16-byte piece of a row of Y: W channels of one token.  kTokens rows of 32
+// channels are a warp's pieces at a time.
 template <bool kF32>
-struct OutType {
+struct Piece {
     using T = float;
+    static constexpr int W = 4;
+    static __device__ __forceinline__ void unpack(const uint4& p, float* f) {
+        f[0] = __uint_as_float(p.x);
+        f[1] = __uint_as_float(p.y);
+        f[2] = __uint_as_float(p.z);
+        f[3] = __uint_as_float(p.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float* f) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                          __float_as_uint(f[3]));
+    }
 };
 template <>
-struct OutType<false> {
+struct Piece<false> {
     using T = __nv_bfloat16;
+    static constexpr int W = 8;
+    static __device__ __forceinline__ void unpack(const uint4& p, float* f) { unpack_bf16x8(p, f); }
+    static __device__ __forceinline__ uint4 pack(const float* f) {
+        uint4 p;
+        uint32_t* w = &p.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return p;
+    }
 };
-__device__ __forceinline__ float load_out(const float* p) { return *p; }
-__device__ __forceinline__ float load_out(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// The next row's address.  The empty asm keeps the compiler from forming every
-// multiple of the row stride ahead of the loops (two registers each).
-template <class T>
-__device__ __forceinline__ void next_row(T*& p, long long ld) {
-    p += ld;
-    asm("" : "+l"(p));
+
+// `here` elements (0 .. W) of a row from p on, one 16-byte access where vec says
+// that all such addresses are 16-byte aligned.
+template <bool kF32>
+__device__ __forceinline__ uint4 load_piece(const typename Piece<kF32>::T* p, int here, bool vec) {
+    using P = Piece<kF32>;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (vec && here == P::W) {
+        v = *reinterpret_cast<const uint4*>(p);
+    } else {
+        typename P::T e[P::W];
+#pragma unroll
+        for (int i = 0; i < P::W; ++i) e[i] = i < here ? p[i] : typename P::T(0.0f);
+        v = *reinterpret_cast<const uint4*>(e);
+    }
+    return v;
+}
+template <bool kF32>
+__device__ __forceinline__ void store_piece(typename Piece<kF32>::T* p, const uint4& v, int here,
+                                            bool vec) {
+    using P = Piece<kF32>;
+    if (vec && here == P::W) {
+        *reinterpret_cast<uint4*>(p) = v;
+    } else {
+        const typename P::T* e = reinterpret_cast<const typename P::T*>(&v);
+#pragma unroll
+        for (int i = 0; i < P::W; ++i)
+            if (i < here) p[i] = e[i];
+    }
 }
 
-// What an epilogue thread keeps of its tile: its channel n, that channel's
-// constants, and where the next token's result and residual are.
-template <class T>
+// What an epilogue thread keeps of its tile: its channel's constants (channel =
+// tensor-memory lane), and the place of its pieces of Y and the residual.
 struct Channel {
-    int n;
+    int n;                   // channel
     float alpha, bias, gate;
-    T* y;
-    const T* r;
+    int piece_here;          // elements of its piece that exist (0 .. W)
+    bool vec_y, vec_r;
 };
-
-// The next C tokens of one channel, accumulators in tensor memory at taddr, all
-// under ch.gate.  The residual's loads are in flight while the accumulators are
-// read.
-template <int C, int kAct, class T>
-__device__ __forceinline__ void epilogue_whole(const MatmulArgs& a, uint32_t taddr, Channel<T>& ch) {
-    uint32_t v[C];
-    tmem_ld16(taddr, v);
-    T res[C];
-    if (a.residual) {
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            res[j] = *ch.r;
-            next_row(ch.r, a.ldr);
-        }
-    }
-    tmem_wait_ld();
-#pragma unroll
-    for (int j = 0; j < C; j += 2) {
-        float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
-                              make_float2(ch.alpha, ch.alpha), make_float2(ch.bias, ch.bias));
-        z = act_pair<kAct>(z);
-        if (a.residual)
-            z = __ffma2_rn(z, make_float2(ch.gate, ch.gate),
-                           make_float2(load_out(&res[j]), load_out(&res[j + 1])));
-        else
-            z = __fmul2_rn(z, make_float2(ch.gate, ch.gate));
-        store_out(ch.y, z.x);
-        next_row(ch.y, a.ldy);
-        store_out(ch.y, z.y);
-        next_row(ch.y, a.ldy);
-    }
-}
-
-// The next `count` (at most 8) tokens from row m on; none where the channel is
-// not stored.  gates: each token's gate is looked up.
-template <int kAct, class T>
-__device__ __forceinline__ void epilogue_ragged(const MatmulArgs& a, uint32_t taddr, Channel<T>& ch,
-                                                int m, int count, bool stored, bool gates) {
-    constexpr int C = 8;
-    uint32_t v[C];
-    tmem_ld8(taddr, v);
-    T res[C];
-    float g[C];
-    int q = 0, rem = 0;
-    if (gates) {
-        q = m / a.rows_per_gate;
-        rem = m - q * a.rows_per_gate;
-    }
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-        const bool here = stored && j < count;
-        g[j] = ch.gate;
-        if (gates) {
-            if (here) g[j] = __ldg(a.gate + (size_t)q * a.N + ch.n);
-            if (++rem == a.rows_per_gate) {
-                rem = 0;
-                ++q;
-            }
-        }
-        if (a.residual) {
-            if (here) res[j] = *ch.r;
-            if (j < count) next_row(ch.r, a.ldr);
-        }
-    }
-    tmem_wait_ld();
-#pragma unroll
-    for (int j = 0; j < C; j += 2) {
-        float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
-                              make_float2(ch.alpha, ch.alpha), make_float2(ch.bias, ch.bias));
-        z = act_pair<kAct>(z);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const bool here = stored && j + k < count;
-            float w = (k ? z.y : z.x) * g[j + k];
-            if (here && a.residual) w = fmaf(k ? z.y : z.x, g[j + k], load_out(&res[j + k]));
-            if (here) store_out(ch.y, w);
-            if (j + k < count) next_row(ch.y, a.ldy);
-        }
-    }
-    __syncwarp();
-}
 
 // One warp's share of a tile: `count` tokens from row m on of 32 channels, their
-// sums in tensor memory from taddr on.
-template <int kAct, bool kGrouped, class T>
+// sums in tensor memory from taddr on.  16 tokens at a time: bias, activation
+// and gate with a thread a channel; then through shared memory to 16-byte pieces
+// of rows, where the residual is added and the result rounded and stored.  The
+// residual of the next 16 tokens is on its way meanwhile (first: of the first).
+template <bool kF32>
+struct Residual {
+    using P = Piece<kF32>;
+    static constexpr int kLanes = 32 / P::W;            // lanes of one token
+    static constexpr int kTokens = 32 / kLanes;         // tokens of one pass
+    static constexpr int kPasses = kChunk / kTokens;
+    uint4 v[kPasses];
+    __device__ __forceinline__ void load(const MatmulArgs& a, int m, int end, int n0, int lane,
+                                         const Channel& ch) {
+        if (!a.residual) return;
+        const int tok = lane / kLanes;
+        const typename P::T* p = static_cast<const typename P::T*>(a.residual) +
+                                 (size_t)(m + tok) * a.ldr + n0 + lane % kLanes * P::W;
+#pragma unroll
+        for (int h = 0; h < kPasses; ++h) {
+            v[h] = load_piece<kF32>(p, tok + kTokens * h < end - m ? ch.piece_here : 0, ch.vec_r);
+            p += kTokens * a.ldr;
+        }
+    }
+};
+
+template <bool kF32, int kAct, bool kGrouped>
 __device__ __forceinline__ void epilogue_share(const MatmulArgs& a, uint32_t taddr, int m, int count,
-                                               Channel<T> ch) {
-    const bool stored = ch.n < a.N;
-    const bool all_stored = __all_sync(0xFFFFFFFFu, stored);
-    // a stretch of tokens under one gate; with fewer than 16 rows a gate, the
-    // gate is looked up token by token
+                                               int n0, int lane, Channel ch, Residual<kF32> res,
+                                               float* stage) {
+    using P = Piece<kF32>;
+    using R = Residual<kF32>;
+    const int end = m + count;
+    const int tok = lane / R::kLanes, col = lane % R::kLanes * P::W;
+    typename P::T* y = static_cast<typename P::T*>(a.Y) + (size_t)(m + tok) * a.ldy + n0 + col;
     const bool by_row = !kGrouped && a.gate;
-    const bool gates = by_row && a.rows_per_gate < 16;
-    int c = 0;
-    while (c < count) {
-        int end = count;
-        if (by_row && !gates) {
-            const int row = (m + c) / a.rows_per_gate;
-            end = (int)min((long long)count, (long long)(row + 1) * a.rows_per_gate - m);
-            ch.gate = stored ? __ldg(a.gate + (size_t)row * a.N + ch.n) : 0.0f;
-        }
-        if (all_stored && !gates) {
 #pragma unroll 1
-            for (; c + 16 <= end; c += 16) epilogue_whole<16, kAct>(a, taddr + c, ch);
+    for (; count > 0; count -= kChunk, m += kChunk, taddr += kChunk) {
+        uint32_t v[kChunk];
+        tmem_ld16(taddr, v);
+        bool one_gate = true;
+        if (by_row) {
+            const int row = m / a.rows_per_gate;
+            one_gate = (min(m + kChunk, end) - 1) / a.rows_per_gate == row;
+            ch.gate = 1.0f;
+            if (one_gate && ch.n < a.N) ch.gate = __ldg(a.gate + (size_t)row * a.N + ch.n);
         }
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < kChunk; j += 2) {
+            float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+                                  make_float2(ch.alpha, ch.alpha), make_float2(ch.bias, ch.bias));
+            z = act_pair<kAct>(z);
+            if (a.gate) z = __fmul2_rn(z, make_float2(ch.gate, ch.gate));
+            stage[j * kEpiRow + lane] = z.x;
+            stage[(j + 1) * kEpiRow + lane] = z.y;
+        }
+        if (!one_gate && ch.n < a.N) {
+            // the chunk's tokens are under several gates: ch.gate is 1 here
 #pragma unroll 1
-        for (; c < end; c += 8)
-            epilogue_ragged<kAct>(a, taddr + c, ch, m + c, min(8, end - c), stored, gates);
-        c = end;
+            for (int j = 0; j < min(kChunk, end - m); ++j)
+                stage[j * kEpiRow + lane] *=
+                    __ldg(a.gate + (size_t)((m + j) / a.rows_per_gate) * a.N + ch.n);
+        }
+        __syncwarp();
+        Residual<kF32> now = res;
+        if (count > kChunk) res.load(a, m + kChunk, end, n0, lane, ch);
+#pragma unroll
+        for (int h = 0; h < R::kPasses; ++h) {
+            const float* row = stage + (tok + R::kTokens * h) * kEpiRow + col;
+            float f[P::W];
+#pragma unroll
+            for (int i = 0; i < P::W; i += 4)
+                *reinterpret_cast<float4*>(f + i) = *reinterpret_cast<const float4*>(row + i);
+            if (a.residual) {
+                float r[P::W];
+                P::unpack(now.v[h], r);
+#pragma unroll
+                for (int i = 0; i < P::W; ++i) f[i] += r[i];
+            }
+            if (tok + R::kTokens * h < end - m)
+                store_piece<kF32>(y, P::pack(f), ch.piece_here, ch.vec_y);
+            y += R::kTokens * a.ldy;
+        }
+        __syncwarp();
     }
 }
 
@@ -614,36 +637,46 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     } else if (warp >= kEpiWarp0) {
         // ------------------------------------------------------------ epilogue
         // warp = lane quarter (warp % 4) of one part of the tile's tokens
-        using T = typename OutType<kF32>::T;
+        using P = Piece<kF32>;
         constexpr int kPart = TN / (kEpiWarps / 4);
         const int first = (warp - kEpiWarp0) / 4 * kPart;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        float* stage = reinterpret_cast<float*>(sf_base + 2 * S::kSfStage) +
+                       (warp - kEpiWarp0) * (kEpiBytes / 4);
+        Channel ch;
+        constexpr int kSize = (int)sizeof(typename P::T);
+        ch.vec_y = ((reinterpret_cast<uintptr_t>(a.Y) | (uintptr_t)(a.ldy * kSize)) & 15u) == 0;
+        ch.vec_r = ((reinterpret_cast<uintptr_t>(a.residual) | (uintptr_t)(a.ldr * kSize)) & 15u) == 0;
         int i = 0;
         for (int t = first_tile; t < total; t += stride, ++i) {
             const TileAt at = tiles.at(t);
             const int buf = i & 1;
             const int m = at.m0 + first;
             const int count = min(kPart, at.m_end - m);
-            Channel<T> ch;
-            ch.n = at.n0 + (warp & 3) * 32 + lane;
+            const int n0 = at.n0 + (warp & 3) * 32;
+            ch.n = n0 + lane;
             const bool nv = ch.n < a.N;
             const size_t en = (size_t)at.e * a.N + ch.n;
             ch.alpha = __ldg(a.x_scale) * __ldg(a.w_scale + at.e);
             ch.bias = (a.bias && nv) ? __ldg(a.bias + en) : 0.0f;
             ch.gate = (a.gate && kGrouped && nv) ? __ldg(a.gate + en) : 1.0f;
-            ch.y = static_cast<T*>(a.Y) + (size_t)m * a.ldy + ch.n;
-            ch.r = static_cast<const T*>(a.residual) + (size_t)m * a.ldr + ch.n;
+            ch.piece_here = max(0, min(P::W, a.N - n0 - lane % (32 / P::W) * P::W));
+            Residual<kF32> res;
+            res.load(a, m, m + count, n0, lane, ch);
             const bool got = wait_or_abort_m(smem_u32(&sh.acc_full[buf]), (uint32_t)((i >> 1) & 1),
                                              abort, a.ctl, 61u, i);
             if (!__all_sync(0xFFFFFFFFu, got)) break;
             tc_fence_after();
             const uint32_t ta = tmem + lane_base + (uint32_t)(buf * TN + first);
             if (a.act == NVFP4KV_ACT_GELU_TANH)
-                epilogue_share<NVFP4KV_ACT_GELU_TANH, kGrouped>(a, ta, m, count, ch);
+                epilogue_share<kF32, NVFP4KV_ACT_GELU_TANH, kGrouped>(a, ta, m, count, n0, lane, ch, res,
+                                                                      stage);
             else if (a.act == NVFP4KV_ACT_SILU)
-                epilogue_share<NVFP4KV_ACT_SILU, kGrouped>(a, ta, m, count, ch);
+                epilogue_share<kF32, NVFP4KV_ACT_SILU, kGrouped>(a, ta, m, count, n0, lane, ch, res,
+                                                                 stage);
             else
-                epilogue_share<NVFP4KV_ACT_NONE, kGrouped>(a, ta, m, count, ch);
+                epilogue_share<kF32, NVFP4KV_ACT_NONE, kGrouped>(a, ta, m, count, n0, lane, ch, res,
+                                                                 stage);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {

@@ -40,7 +40,8 @@ namespace {
 constexpr int kTileN = 128;                 // output channels of a tile (the MMA's M)
 constexpr int kStageK = 256;                // elements along k of one stage
 constexpr int kThreadsMM = 512;
-constexpr int kScaleWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kEpiWarp0 = 8, kEpiWarps = 8;   // 6, 7: idle
+constexpr int kScaleWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kEpiWarp0 = 8, kEpiWarps = 8;
+constexpr int kPrefetchWarp = 6;            // (7: idle)
 constexpr int kColsMM = 512;                // tensor-memory columns
 constexpr int kATile = kTileN * 128;        // bytes of codes of a weight tile's stage
 // Scales travel in turns of 4 steps; a K = 64 block of a 128-row group takes 512
@@ -48,10 +49,6 @@ constexpr int kATile = kTileN * 128;        // bytes of codes of a weight tile's
 constexpr int kTurn = 4;
 constexpr int kSfBlock = 512 + 16;
 constexpr int kSfGroup = 4 * kTurn * kSfBlock;
-constexpr int kChunk = 16;              // tokens an epilogue warp takes at a time
-constexpr int kEpiRow = 36;             // floats from one token's 32 channels to the next's:
-                                        // 16-byte reads of two rows fall in different banks
-constexpr int kEpiBytes = kChunk * kEpiRow * 4;
 constexpr int kMaxStages = 12;
 constexpr unsigned long long kLandNs = 10ull * 1000 * 1000;   // 10 ms
 constexpr size_t kStageRoom = 216 * 1024;    // of 227 KB; the rest: offsets, barriers, alignment
@@ -83,9 +80,9 @@ struct Shape {
     static constexpr int kStage = kATile + kBTile;
     static constexpr int kGroups = 1 + (TN + 127) / 128;     // 128-row groups of scales
     static constexpr int kSfStage = kGroups * kSfGroup;
-    static constexpr int kFit = (int)((kStageRoom - 2 * kSfStage - kEpiWarps * kEpiBytes) / kStage);
+    static constexpr int kFit = (int)((kStageRoom - 2 * kSfStage) / kStage);
     static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
-    static constexpr size_t kSmem = (size_t)kStages * kStage + 2 * kSfStage + kEpiWarps * kEpiBytes + 1024;
+    static constexpr size_t kSmem = (size_t)kStages * kStage + 2 * kSfStage + 1024;
     static_assert(kStage % 1024 == 0, "stages keep the swizzle alignment");
     static constexpr uint32_t kColSFA = 2 * TN, kColSFB = 2 * TN + 16;   // 16 and up to 32 columns
     static_assert(2 * TN + 16 + 8 * 4 <= kColsMM, "two accumulators beside the scales");
@@ -113,6 +110,12 @@ __device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// Arrive on the leader's barrier (for one CTA, its own).
+template <int G>
+__device__ __forceinline__ void arrive_leader(uint32_t mbar) {
+    if (G == 1) mbar_arrive(mbar);
+    else mbar_arrive_cluster(leader_addr(mbar));
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
@@ -263,165 +266,151 @@ __device__ __forceinline__ float2 act_pair(float2 z) {
     return __fmul2_rn(z, __fmul2_rn(make_float2(d.y, d.x), make_float2(r, r)));
 }
 
-// A 16-byte piece of a row of Y: W channels of one token.  kTokens rows of 32
-// channels are a warp's pieces at a time.
 template <bool kF32>
-struct Piece {
+struct OutType {
     using T = float;
-    static constexpr int W = 4;
-    static __device__ __forceinline__ void unpack(const uint4& p, float* f) {
-        f[0] = __uint_as_float(p.x);
-        f[1] = __uint_as_float(p.y);
-        f[2] = __uint_as_float(p.z);
-        f[3] = __uint_as_float(p.w);
-    }
-    static __device__ __forceinline__ uint4 pack(const float* f) {
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                          __float_as_uint(f[3]));
-    }
 };
 template <>
-struct Piece<false> {
+struct OutType<false> {
     using T = __nv_bfloat16;
-    static constexpr int W = 8;
-    static __device__ __forceinline__ void unpack(const uint4& p, float* f) { unpack_bf16x8(p, f); }
-    static __device__ __forceinline__ uint4 pack(const float* f) {
-        uint4 p;
-        uint32_t* w = &p.x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        return p;
-    }
 };
+__device__ __forceinline__ float load_out(const float* p) { return *p; }
+__device__ __forceinline__ float load_out(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-
-// `here` elements (0 .. W) of a row from p on, one 16-byte access where vec says
-// that all such addresses are 16-byte aligned.
-template <bool kF32>
-__device__ __forceinline__ uint4 load_piece(const typename Piece<kF32>::T* p, int here, bool vec) {
-    using P = Piece<kF32>;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (vec && here == P::W) {
-        v = *reinterpret_cast<const uint4*>(p);
-    } else {
-        typename P::T e[P::W];
-#pragma unroll
-        for (int i = 0; i < P::W; ++i) e[i] = i < here ? p[i] : typename P::T(0.0f);
-        v = *reinterpret_cast<const uint4*>(e);
-    }
-    return v;
-}
-template <bool kF32>
-__device__ __forceinline__ void store_piece(typename Piece<kF32>::T* p, const uint4& v, int here,
-                                            bool vec) {
-    using P = Piece<kF32>;
-    if (vec && here == P::W) {
-        *reinterpret_cast<uint4*>(p) = v;
-    } else {
-        const typename P::T* e = reinterpret_cast<const typename P::T*>(&v);
-#pragma unroll
-        for (int i = 0; i < P::W; ++i)
-            if (i < here) p[i] = e[i];
-    }
+// The next row's address.  The empty asm keeps the compiler from forming every
+// multiple of the row stride ahead of the loops (two registers each).
+template <class T>
+__device__ __forceinline__ void next_row(T*& p, long long ld) {
+    p += ld;
+    asm("" : "+l"(p));
 }
 
-// What an epilogue thread keeps of its tile: its channel's constants (channel =
-// tensor-memory lane), and the place of its pieces of Y and the residual.
+// What an epilogue thread keeps of its tile: its channel n, that channel's
+// constants, and where the next token's result and residual are.
+template <class T>
 struct Channel {
-    int n;                   // channel
+    int n;
+    bool stored;             // n < N
     float alpha, bias, gate;
-    int piece_here;          // elements of its piece that exist (0 .. W)
-    bool vec_y, vec_r;
+    T* y;
+    const T* r;
 };
 
-// One warp's share of a tile: `count` tokens from row m on of 32 channels, their
-// sums in tensor memory from taddr on.  16 tokens at a time: bias, activation
-// and gate with a thread a channel; then through shared memory to 16-byte pieces
-// of rows, where the residual is added and the result rounded and stored.  The
-// residual of the next 16 tokens is on its way meanwhile (first: of the first).
-template <bool kF32>
-struct Residual {
-    using P = Piece<kF32>;
-    static constexpr int kLanes = 32 / P::W;            // lanes of one token
-    static constexpr int kTokens = 32 / kLanes;         // tokens of one pass
-    static constexpr int kPasses = kChunk / kTokens;
-    uint4 v[kPasses];
-    __device__ __forceinline__ void load(const MatmulArgs& a, int m, int end, int n0, int lane,
-                                         const Channel& ch) {
-        if (!a.residual) return;
-        const int tok = lane / kLanes;
-        const typename P::T* p = static_cast<const typename P::T*>(a.residual) +
-                                 (size_t)(m + tok) * a.ldr + n0 + lane % kLanes * P::W;
+constexpr int kChunk = 16;      // tokens an epilogue warp takes at a time
+
+// The residual of the next C tokens, `count` of which exist.
+template <int C, class T>
+__device__ __forceinline__ void load_residual(const MatmulArgs& a, Channel<T>& ch, T* res, int count) {
 #pragma unroll
-        for (int h = 0; h < kPasses; ++h) {
-            v[h] = load_piece<kF32>(p, tok + kTokens * h < end - m ? ch.piece_here : 0, ch.vec_r);
-            p += kTokens * a.ldr;
-        }
+    for (int j = 0; j < C; ++j) {
+        if (j < count) res[j] = *ch.r;
+        next_row(ch.r, a.ldr);
     }
-};
+}
 
-template <bool kF32, int kAct, bool kGrouped>
-__device__ __forceinline__ void epilogue_share(const MatmulArgs& a, uint32_t taddr, int m, int count,
-                                               int n0, int lane, Channel ch, Residual<kF32> res,
-                                               float* stage) {
-    using P = Piece<kF32>;
-    using R = Residual<kF32>;
-    const int end = m + count;
-    const int tok = lane / R::kLanes, col = lane % R::kLanes * P::W;
-    typename P::T* y = static_cast<typename P::T*>(a.Y) + (size_t)(m + tok) * a.ldy + n0 + col;
-    const bool by_row = !kGrouped && a.gate;
+// The next C tokens of one channel, `count` of which exist, from their sums v and
+// residual res; the gates are g[0 .. C) where kGates, else g[0].
+template <int C, int kAct, bool kRes, bool kGates, class T>
+__device__ __forceinline__ void finish_tokens(const MatmulArgs& a, const uint32_t* v, const T* res,
+                                              Channel<T>& ch, int count, const float* g) {
+#pragma unroll
+    for (int j = 0; j < C; j += 2) {
+        float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+                              make_float2(ch.alpha, ch.alpha), make_float2(ch.bias, ch.bias));
+        z = act_pair<kAct>(z);
+        const float2 gg = kGates ? make_float2(g[j], g[j + 1]) : make_float2(g[0], g[0]);
+        if (kRes) z = __ffma2_rn(z, gg, make_float2(load_out(&res[j]), load_out(&res[j + 1])));
+        else z = __fmul2_rn(z, gg);
+        if (j < count) store_out(ch.y, z.x);
+        next_row(ch.y, a.ldy);
+        if (j + 1 < count) store_out(ch.y, z.y);
+        next_row(ch.y, a.ldy);
+    }
+}
+
+// `count` tokens of one channel, accumulators in tensor memory at taddr, all under
+// ch.gate; the next 16's residual is on its way meanwhile.  Leaves ch.y and ch.r
+// behind the last token.
+template <int kAct, bool kRes, class T>
+__device__ __forceinline__ void epilogue_run(const MatmulArgs& a, uint32_t taddr, Channel<T>& ch,
+                                             int count) {
+    T next[kRes ? kChunk : 1];
+    T* const y_end = ch.y + (size_t)count * a.ldy;
+    const T* const r_end = ch.r + (size_t)count * a.ldr;
+    const int here = ch.stored ? 0 : -(1 << 20);      // tokens of no stored channel: none
+    if (kRes) load_residual<kChunk>(a, ch, next, count + here);
 #pragma unroll 1
-    for (; count > 0; count -= kChunk, m += kChunk, taddr += kChunk) {
+    for (; count > 0; count -= kChunk, taddr += kChunk) {
         uint32_t v[kChunk];
         tmem_ld16(taddr, v);
-        bool one_gate = true;
-        if (by_row) {
-            const int row = m / a.rows_per_gate;
-            one_gate = (min(m + kChunk, end) - 1) / a.rows_per_gate == row;
-            ch.gate = 1.0f;
-            if (one_gate && ch.n < a.N) ch.gate = __ldg(a.gate + (size_t)row * a.N + ch.n);
+        T res[kRes ? kChunk : 1];
+        if (kRes) {
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) res[j] = next[j];
+            load_residual<kChunk>(a, ch, next, count - kChunk + here);
         }
         tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < kChunk; j += 2) {
-            float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
-                                  make_float2(ch.alpha, ch.alpha), make_float2(ch.bias, ch.bias));
-            z = act_pair<kAct>(z);
-            if (a.gate) z = __fmul2_rn(z, make_float2(ch.gate, ch.gate));
-            stage[j * kEpiRow + lane] = z.x;
-            stage[(j + 1) * kEpiRow + lane] = z.y;
-        }
-        if (!one_gate && ch.n < a.N) {
-            // the chunk's tokens are under several gates: ch.gate is 1 here
+        finish_tokens<kChunk, kAct, kRes, false>(a, v, res, ch, count + here, &ch.gate);
+    }
+    ch.y = y_end;
+    ch.r = r_end;
+}
+
+// `count` tokens from row m on, their gates looked up one by one.
+template <int kAct, class T>
+__device__ __forceinline__ void epilogue_gates(const MatmulArgs& a, uint32_t taddr, Channel<T>& ch, int m,
+                                               int count) {
+    constexpr int C = 4;
+    int q = m / a.rows_per_gate, rem = m - q * a.rows_per_gate;
 #pragma unroll 1
-            for (int j = 0; j < min(kChunk, end - m); ++j)
-                stage[j * kEpiRow + lane] *=
-                    __ldg(a.gate + (size_t)((m + j) / a.rows_per_gate) * a.N + ch.n);
-        }
-        __syncwarp();
-        Residual<kF32> now = res;
-        if (count > kChunk) res.load(a, m + kChunk, end, n0, lane, ch);
+    for (; count > 0; count -= C, taddr += C) {
+        const int here = ch.stored ? count : 0;
+        uint32_t v[C];
+        tmem_ld4(taddr, v);
+        T res[C] = {T(0.0f), T(0.0f), T(0.0f), T(0.0f)};
+        if (a.residual) load_residual<C>(a, ch, res, here);
+        float g[C];
 #pragma unroll
-        for (int h = 0; h < R::kPasses; ++h) {
-            const float* row = stage + (tok + R::kTokens * h) * kEpiRow + col;
-            float f[P::W];
-#pragma unroll
-            for (int i = 0; i < P::W; i += 4)
-                *reinterpret_cast<float4*>(f + i) = *reinterpret_cast<const float4*>(row + i);
-            if (a.residual) {
-                float r[P::W];
-                P::unpack(now.v[h], r);
-#pragma unroll
-                for (int i = 0; i < P::W; ++i) f[i] += r[i];
+        for (int j = 0; j < C; ++j) {
+            if (j < here) g[j] = __ldg(a.gate + (size_t)q * a.N + ch.n);
+            if (++rem == a.rows_per_gate) {
+                rem = 0;
+                ++q;
             }
-            if (tok + R::kTokens * h < end - m)
-                store_piece<kF32>(y, P::pack(f), ch.piece_here, ch.vec_y);
-            y += R::kTokens * a.ldy;
         }
+        tmem_wait_ld();
+        finish_tokens<C, kAct, true, true>(a, v, res, ch, here, g);
         __syncwarp();
+    }
+}
+
+// One warp's share of a tile: `count` tokens from row m on of 32 channels, their
+// sums in tensor memory from taddr on.  Gates of 16 rows or more are taken a
+// stretch of tokens under one gate at a time.
+template <int kAct, bool kGrouped, class T>
+__device__ __forceinline__ void epilogue_share(const MatmulArgs& a, uint32_t taddr, int m, int count,
+                                               Channel<T> ch) {
+    const bool by_row = !kGrouped && a.gate;
+    if (by_row && a.rows_per_gate < kChunk) {
+        epilogue_gates<kAct>(a, taddr, ch, m, count);
+        return;
+    }
+#pragma unroll 1
+    while (count > 0) {
+        int n = count;
+        if (by_row) {
+            const int row = m / a.rows_per_gate;
+            n = (int)min((long long)count, (long long)(row + 1) * a.rows_per_gate - m);
+            if (ch.stored) ch.gate = __ldg(a.gate + (size_t)row * a.N + ch.n);
+        }
+        if (a.residual) epilogue_run<kAct, true>(a, taddr, ch, n);
+        else epilogue_run<kAct, false>(a, taddr, ch, n);
+        __syncwarp();
+        taddr += n;
+        m += n;
+        count -= n;
     }
 }
 
@@ -502,7 +491,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             mbar_init(smem_u32(&sh.sf_full[i]), kScaleWarps * G);
             mbar_init(smem_u32(&sh.sf_empty[i]), 1);
             mbar_init(smem_u32(&sh.acc_full[i]), 1);
-            mbar_init(smem_u32(&sh.acc_free[i]), kEpiWarps * G);
+            mbar_init(smem_u32(&sh.acc_free[i]), (kEpiWarps + (a.residual ? 1 : 0)) * G);
         }
         mbar_init(smem_u32(&sh.drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -626,10 +615,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 put(sf_base + st * S::kSfStage);
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0 && !(withhold && it == 0)) {
-                    if (G == 1) mbar_arrive(smem_u32(&sh.sf_full[st]));
-                    else mbar_arrive_cluster(leader_addr(smem_u32(&sh.sf_full[st])));
-                }
+                if (lane == 0 && !(withhold && it == 0)) arrive_leader<G>(smem_u32(&sh.sf_full[st]));
                 if (turn + 1 < turns) fetch(at, turn + 1);
                 else if (t + stride < total) fetch(tiles.at(t + stride), 0);
             }
@@ -637,52 +623,39 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     } else if (warp >= kEpiWarp0) {
         // ------------------------------------------------------------ epilogue
         // warp = lane quarter (warp % 4) of one part of the tile's tokens
-        using P = Piece<kF32>;
+        using T = typename OutType<kF32>::T;
         constexpr int kPart = TN / (kEpiWarps / 4);
         const int first = (warp - kEpiWarp0) / 4 * kPart;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        float* stage = reinterpret_cast<float*>(sf_base + 2 * S::kSfStage) +
-                       (warp - kEpiWarp0) * (kEpiBytes / 4);
-        Channel ch;
-        constexpr int kSize = (int)sizeof(typename P::T);
-        ch.vec_y = ((reinterpret_cast<uintptr_t>(a.Y) | (uintptr_t)(a.ldy * kSize)) & 15u) == 0;
-        ch.vec_r = ((reinterpret_cast<uintptr_t>(a.residual) | (uintptr_t)(a.ldr * kSize)) & 15u) == 0;
         int i = 0;
         for (int t = first_tile; t < total; t += stride, ++i) {
             const TileAt at = tiles.at(t);
             const int buf = i & 1;
             const int m = at.m0 + first;
             const int count = min(kPart, at.m_end - m);
-            const int n0 = at.n0 + (warp & 3) * 32;
-            ch.n = n0 + lane;
-            const bool nv = ch.n < a.N;
+            Channel<T> ch;
+            ch.n = at.n0 + (warp & 3) * 32 + lane;
+            ch.stored = ch.n < a.N;
             const size_t en = (size_t)at.e * a.N + ch.n;
             ch.alpha = __ldg(a.x_scale) * __ldg(a.w_scale + at.e);
-            ch.bias = (a.bias && nv) ? __ldg(a.bias + en) : 0.0f;
-            ch.gate = (a.gate && kGrouped && nv) ? __ldg(a.gate + en) : 1.0f;
-            ch.piece_here = max(0, min(P::W, a.N - n0 - lane % (32 / P::W) * P::W));
-            Residual<kF32> res;
-            res.load(a, m, m + count, n0, lane, ch);
+            ch.bias = (a.bias && ch.stored) ? __ldg(a.bias + en) : 0.0f;
+            ch.gate = (a.gate && kGrouped && ch.stored) ? __ldg(a.gate + en) : 1.0f;
+            ch.y = static_cast<T*>(a.Y) + (size_t)m * a.ldy + ch.n;
+            ch.r = static_cast<const T*>(a.residual) + (size_t)m * a.ldr + ch.n;
             const bool got = wait_or_abort_m(smem_u32(&sh.acc_full[buf]), (uint32_t)((i >> 1) & 1),
                                              abort, a.ctl, 61u, i);
             if (!__all_sync(0xFFFFFFFFu, got)) break;
             tc_fence_after();
             const uint32_t ta = tmem + lane_base + (uint32_t)(buf * TN + first);
             if (a.act == NVFP4KV_ACT_GELU_TANH)
-                epilogue_share<kF32, NVFP4KV_ACT_GELU_TANH, kGrouped>(a, ta, m, count, n0, lane, ch, res,
-                                                                      stage);
+                epilogue_share<NVFP4KV_ACT_GELU_TANH, kGrouped>(a, ta, m, count, ch);
             else if (a.act == NVFP4KV_ACT_SILU)
-                epilogue_share<kF32, NVFP4KV_ACT_SILU, kGrouped>(a, ta, m, count, n0, lane, ch, res,
-                                                                 stage);
+                epilogue_share<NVFP4KV_ACT_SILU, kGrouped>(a, ta, m, count, ch);
             else
-                epilogue_share<kF32, NVFP4KV_ACT_NONE, kGrouped>(a, ta, m, count, n0, lane, ch, res,
-                                                                 stage);
+                epilogue_share<NVFP4KV_ACT_NONE, kGrouped>(a, ta, m, count, ch);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                if (G == 1) mbar_arrive(smem_u32(&sh.acc_free[buf]));
-                else mbar_arrive_cluster(leader_addr(smem_u32(&sh.acc_free[buf])));
-            }
+            if (lane == 0) arrive_leader<G>(smem_u32(&sh.acc_free[buf]));
         }
     } else if (warp == kTmaWarp) {
         // ------------------------------------------------------------ code tiles
@@ -721,6 +694,32 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             }
         }
         __syncwarp();
+    } else if (warp == kPrefetchWarp && a.residual) {
+        // ------------------------------------------------------------ residual
+        // Each tile's residual into L2 while its sums are formed: the epilogue
+        // then waits for L2, not for HBM.  A step ahead of the epilogue, which
+        // it may not outrun (it takes part in freeing the accumulators).
+        constexpr int kSize = kF32 ? 4 : 2;
+        const char* res = static_cast<const char*>(a.residual);
+        int i = 0;
+        for (int t = first_tile; t < total; t += stride, ++i) {
+            const TileAt at = tiles.at(t);
+            const int bytes = min(kTileN, a.N - at.n0) * kSize;
+            constexpr int kLines = kTileN * kSize / 128;      // lanes of a row
+            for (int r = lane / kLines; r < at.m_end - at.m0; r += 32 / kLines) {
+                const int b = lane % kLines * 128;
+                if (b < bytes)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                        res + ((size_t)(at.m0 + r) * a.ldr + at.n0) * kSize + b));
+            }
+            if (i > 0) {
+                const bool got = wait_or_abort_m(smem_u32(&sh.acc_full[(i - 1) & 1]),
+                                                 (uint32_t)(((i - 1) >> 1) & 1), abort, a.ctl, 67u, i);
+                if (!__all_sync(0xFFFFFFFFu, got)) break;
+                if (lane == 0) arrive_leader<G>(smem_u32(&sh.acc_free[(i - 1) & 1]));
+            }
+        }
+        if (i > 0 && lane == 0) arrive_leader<G>(smem_u32(&sh.acc_free[(i - 1) & 1]));
     } else if (warp == kMmaWarp && rank == 0) {
         // ------------------------------------------------------------ MMA issue
         // One elected lane walks the steps.  (elect.sync, not lane == 0: knowing

@@ -42,6 +42,9 @@ constexpr int kStageK = 256;                // elements along k of one stage
 constexpr int kThreadsMM = 512;
 constexpr int kScaleWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kEpiWarp0 = 8, kEpiWarps = 8;
 constexpr int kPrefetchWarp = 6;            // (7: idle)
+// Registers of a thread: 128 at launch (65536 / 512); 104 for the first two
+// warpgroups and 152 for the epilogue's two: 256 * 104 + 256 * 152 = 65536.
+constexpr int kFewRegs = 104, kManyRegs = 152;
 constexpr int kColsMM = 512;                // tensor-memory columns
 constexpr int kATile = kTileN * 128;        // bytes of codes of a weight tile's stage
 // Scales travel in turns of 4 steps; a K = 64 block of a 128-row group takes 512
@@ -279,13 +282,25 @@ __device__ __forceinline__ float load_out(const __nv_bfloat16* p) { return __bfl
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// The next row's address.  The empty asm keeps the compiler from forming every
-// multiple of the row stride ahead of the loops (two registers each).
+// Walks down the rows of one channel.  Four addresses take turns, each stepping
+// four rows, so that a row does not wait for the 64-bit addition of the row
+// before; the empty asm keeps the compiler from forming every multiple of the
+// row stride ahead of the loops (two registers each).
 template <class T>
-__device__ __forceinline__ void next_row(T*& p, long long ld) {
-    p += ld;
-    asm("" : "+l"(p));
-}
+struct Walk {
+    T* p[4];
+    __device__ __forceinline__ Walk(T* first, long long ld) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = first + i * ld;
+    }
+    // the address of row j (rows in order, j known at compile time)
+    __device__ __forceinline__ T* row(int j, long long ld) {
+        T* r = p[j & 3];
+        p[j & 3] += 4 * ld;
+        asm("" : "+l"(p[j & 3]));
+        return r;
+    }
+};
 
 // What an epilogue thread keeps of its tile: its channel n, that channel's
 // constants, and where the next token's result and residual are.
@@ -302,11 +317,11 @@ constexpr int kChunk = 16;      // tokens an epilogue warp takes at a time
 
 // The residual of the next C tokens, `count` of which exist.
 template <int C, class T>
-__device__ __forceinline__ void load_residual(const MatmulArgs& a, Channel<T>& ch, T* res, int count) {
+__device__ __forceinline__ void load_residual(const MatmulArgs& a, Walk<const T>& r, T* res, int count) {
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-        if (j < count) res[j] = *ch.r;
-        next_row(ch.r, a.ldr);
+        const T* p = r.row(j, a.ldr);
+        if (j < count) res[j] = *p;
     }
 }
 
@@ -314,7 +329,8 @@ __device__ __forceinline__ void load_residual(const MatmulArgs& a, Channel<T>& c
 // residual res; the gates are g[0 .. C) where kGates, else g[0].
 template <int C, int kAct, bool kRes, bool kGates, class T>
 __device__ __forceinline__ void finish_tokens(const MatmulArgs& a, const uint32_t* v, const T* res,
-                                              Channel<T>& ch, int count, const float* g) {
+                                              const Channel<T>& ch, Walk<T>& y, int count,
+                                              const float* g) {
 #pragma unroll
     for (int j = 0; j < C; j += 2) {
         float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
@@ -323,10 +339,10 @@ __device__ __forceinline__ void finish_tokens(const MatmulArgs& a, const uint32_
         const float2 gg = kGates ? make_float2(g[j], g[j + 1]) : make_float2(g[0], g[0]);
         if (kRes) z = __ffma2_rn(z, gg, make_float2(load_out(&res[j]), load_out(&res[j + 1])));
         else z = __fmul2_rn(z, gg);
-        if (j < count) store_out(ch.y, z.x);
-        next_row(ch.y, a.ldy);
-        if (j + 1 < count) store_out(ch.y, z.y);
-        next_row(ch.y, a.ldy);
+        T* y0 = y.row(j, a.ldy);
+        T* y1 = y.row(j + 1, a.ldy);
+        if (j < count) store_out(y0, z.x);
+        if (j + 1 < count) store_out(y1, z.y);
     }
 }
 
@@ -337,10 +353,12 @@ template <int kAct, bool kRes, class T>
 __device__ __forceinline__ void epilogue_run(const MatmulArgs& a, uint32_t taddr, Channel<T>& ch,
                                              int count) {
     T next[kRes ? kChunk : 1];
-    T* const y_end = ch.y + (size_t)count * a.ldy;
-    const T* const r_end = ch.r + (size_t)count * a.ldr;
+    Walk<T> y(ch.y, a.ldy);
+    Walk<const T> r(ch.r, kRes ? a.ldr : 0);
+    ch.y += (size_t)count * a.ldy;
+    if (kRes) ch.r += (size_t)count * a.ldr;
     const int here = ch.stored ? 0 : -(1 << 20);      // tokens of no stored channel: none
-    if (kRes) load_residual<kChunk>(a, ch, next, count + here);
+    if (kRes) load_residual<kChunk>(a, r, next, count + here);
 #pragma unroll 1
     for (; count > 0; count -= kChunk, taddr += kChunk) {
         uint32_t v[kChunk];
@@ -349,13 +367,11 @@ __device__ __forceinline__ void epilogue_run(const MatmulArgs& a, uint32_t taddr
         if (kRes) {
 #pragma unroll
             for (int j = 0; j < kChunk; ++j) res[j] = next[j];
-            load_residual<kChunk>(a, ch, next, count - kChunk + here);
+            load_residual<kChunk>(a, r, next, count - kChunk + here);
         }
         tmem_wait_ld();
-        finish_tokens<kChunk, kAct, kRes, false>(a, v, res, ch, count + here, &ch.gate);
+        finish_tokens<kChunk, kAct, kRes, false>(a, v, res, ch, y, count + here, &ch.gate);
     }
-    ch.y = y_end;
-    ch.r = r_end;
 }
 
 // `count` tokens from row m on, their gates looked up one by one.
@@ -363,6 +379,8 @@ template <int kAct, class T>
 __device__ __forceinline__ void epilogue_gates(const MatmulArgs& a, uint32_t taddr, Channel<T>& ch, int m,
                                                int count) {
     constexpr int C = 4;
+    Walk<T> y(ch.y, a.ldy);
+    Walk<const T> r(ch.r, a.ldr);
     int q = m / a.rows_per_gate, rem = m - q * a.rows_per_gate;
 #pragma unroll 1
     for (; count > 0; count -= C, taddr += C) {
@@ -370,7 +388,7 @@ __device__ __forceinline__ void epilogue_gates(const MatmulArgs& a, uint32_t tad
         uint32_t v[C];
         tmem_ld4(taddr, v);
         T res[C] = {T(0.0f), T(0.0f), T(0.0f), T(0.0f)};
-        if (a.residual) load_residual<C>(a, ch, res, here);
+        if (a.residual) load_residual<C>(a, r, res, here);
         float g[C];
 #pragma unroll
         for (int j = 0; j < C; ++j) {
@@ -381,7 +399,7 @@ __device__ __forceinline__ void epilogue_gates(const MatmulArgs& a, uint32_t tad
             }
         }
         tmem_wait_ld();
-        finish_tokens<C, kAct, true, true>(a, v, res, ch, here, g);
+        finish_tokens<C, kAct, true, true>(a, v, res, ch, y, here, g);
         __syncwarp();
     }
 }
@@ -542,6 +560,10 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     const int kbytes = a.K / 16;
     uint8_t* sf_base = base + (size_t)S::kStages * S::kStage;
 
+    if (warp < kEpiWarp0)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    else
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
     if (warp < kTmaWarp) {
         // ------------------------------------------------------------ block scales
         // Per turn, 4 steps (64 scale bytes a row) of every 128-row group.  Unit u

@@ -27,7 +27,9 @@
 // (32x128b.warpx4) places in 4 columns of every lane quarter.
 #include <cuda.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -46,6 +48,7 @@ constexpr int kPrefetchWarp = 6;            // (7: idle)
 // warpgroups and 152 for the epilogue's two: 256 * 104 + 256 * 152 = 65536.
 constexpr int kFewRegs = 104, kManyRegs = 152;
 constexpr int kColsMM = 512;                // tensor-memory columns
+constexpr int kBox = 32;                    // token rows of one TMA load
 constexpr int kATile = kTileN * 128;        // bytes of codes of a weight tile's stage
 // Scales travel in turns of 4 steps; a K = 64 block of a 128-row group takes 512
 // bytes, 16 more apart so that a warp's 16-byte lines fall in different banks.
@@ -89,7 +92,7 @@ struct Shape {
     static_assert(kStage % 1024 == 0, "stages keep the swizzle alignment");
     static constexpr uint32_t kColSFA = 2 * TN, kColSFB = 2 * TN + 16;   // 16 and up to 32 columns
     static_assert(2 * TN + 16 + 8 * 4 <= kColsMM, "two accumulators beside the scales");
-    static_assert(TN / G % 8 == 0, "whole swizzle atoms of token rows");
+    static_assert(TN / G % kBox == 0, "whole loads of token rows");
 };
 
 struct MMShared {
@@ -433,18 +436,30 @@ __device__ __forceinline__ void epilogue_share(const MatmulArgs& a, uint32_t tad
 }
 
 struct TileAt {
-    int e, n0, m0, m_end;
+    int e, n0, m0, m_end;    // expert, first channel, rows [m0, m_end)
+    int tokens;              // m_end - m0 rounded up to 16: the MMA's N
 };
+
+// Rows of a tile of a group of `rows` > 0: as few tiles as TN allows, of one size,
+// a multiple of 16 (the last may be shorter).
+template <int TN>
+__host__ __device__ __forceinline__ int tile_rows(int rows) {
+    const int count = (rows + TN - 1) / TN;
+    return ((rows + count - 1) / count + 15) / 16 * 16;
+}
 
 template <int TN, int G, bool kGrouped>
 struct Tiles {
     const MatmulArgs& a;
-    const int* s_off;
+    const int* s_off;        // grouped: row offsets, first tiles and tile rows of the groups
     const int* s_tile;
-    int n_tiles, e, rank;
-    __device__ Tiles(const MatmulArgs& args, const int* off, const int* tile, int rank_)
-        : a(args), s_off(off), s_tile(tile), e(0), rank(rank_) {
+    const int* s_size;
+    int n_tiles, e, rank, size;
+    __device__ Tiles(const MatmulArgs& args, const int* off, const int* tile, const int* sizes,
+                     int rank_)
+        : a(args), s_off(off), s_tile(tile), s_size(sizes), e(0), rank(rank_) {
         n_tiles = (a.N + kTileN * G - 1) / (kTileN * G);
+        size = kGrouped ? 0 : tile_rows<TN>(a.M);
     }
     __device__ int total() const {
         return kGrouped ? s_tile[a.E] : ((a.M + TN - 1) / TN) * n_tiles;
@@ -452,18 +467,20 @@ struct Tiles {
     // t grows from call to call
     __device__ TileAt at(int t) {
         TileAt r;
-        int row0 = 0, m_end = a.M;
+        int row0 = 0, m_end = a.M;        // the group's rows
         if (kGrouped) {
             while (s_tile[e + 1] <= t) ++e;
             t -= s_tile[e];
             row0 = s_off[e];
             m_end = s_off[e + 1];
+            size = s_size[e];
         }
         const int mt = t / n_tiles;
         r.e = e;
         r.n0 = ((t - mt * n_tiles) * G + rank) * kTileN;   // this CTA's channels
-        r.m0 = row0 + mt * TN;
-        r.m_end = min(m_end, r.m0 + TN);
+        r.m0 = row0 + mt * size;
+        r.m_end = min(m_end, r.m0 + size);
+        r.tokens = (r.m_end - r.m0 + 15) / 16 * 16;
         return r;
     }
 };
@@ -477,6 +494,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     __shared__ MMShared sh;
     __shared__ int s_off[kGrouped ? kMaxExperts + 1 : 1];
     __shared__ int s_tile[kGrouped ? kMaxExperts + 1 : 1];
+    __shared__ int s_size[kGrouped ? kMaxExperts : 1];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort = &sh.abort;
@@ -529,6 +547,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 s_off[e] = o0;
                 if (e == a.E - 1) s_off[a.E] = o1;
                 cnt = ((o1 - o0 + TN - 1) / TN) * nt;
+                s_size[e] = o1 > o0 ? tile_rows<TN>(o1 - o0) : 0;
             }
             int inc = cnt;
 #pragma unroll
@@ -553,7 +572,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     if (G == 2) cluster_sync();      // both CTAs' barriers are ready
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
-    Tiles<TN, G, kGrouped> tiles(a, s_off, s_tile, rank);
+    Tiles<TN, G, kGrouped> tiles(a, s_off, s_tile, s_size, rank);
     const int total = tiles.total();
     const int steps = (a.K + kStageK - 1) / kStageK;
     const int turns = (steps + kTurn - 1) / kTurn;
@@ -584,7 +603,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             const uint8_t* xp = a.x_scales + kb;
             if (wide) {
                 const int n_end = kb < kbytes ? a.N : 0;
-                const int m_end = kb < kbytes ? min(at.m_end, at.m0 + TN) : 0;
+                const int m_end = kb < kbytes ? at.m_end : 0;
                 // rows 8 apart; in tiles rows 16 apart have scale rows 1 apart
                 // (n0 is a multiple of 16)
                 const uint8_t* p = wp + (size_t)(nw >> a.w_shift) * kbytes;
@@ -600,13 +619,12 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                     p += (u & 3) == 3 ? 104 * kbytes : 8 * kbytes;
                 }
             } else {
-                const int m_end = min(at.m_end, at.m0 + TN);
 #pragma unroll
                 for (int u = 0; u < kUnits; ++u) {
                     const int i = (u < 4 ? nw : mx + 128 * (u / 4 - 1)) + 8 * (u & 3);
                     const uint8_t* p = (u < 4 ? wp : xp) +
                                        (size_t)(i >> (u < 4 ? a.w_shift : a.x_shift)) * kbytes;
-                    const int left = i < (u < 4 ? a.N : m_end) ? kbytes - kb : 0;
+                    const int left = i < (u < 4 ? a.N : at.m_end) ? kbytes - kb : 0;
                     w[u] = make_uint4(scale_word(p, left), scale_word(p + 4, left - 4),
                                       scale_word(p + 8, left - 8), scale_word(p + 12, left - 12));
                 }
@@ -646,15 +664,16 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         // ------------------------------------------------------------ epilogue
         // warp = lane quarter (warp % 4) of one part of the tile's tokens
         using T = typename OutType<kF32>::T;
-        constexpr int kPart = TN / (kEpiWarps / 4);
-        const int first = (warp - kEpiWarp0) / 4 * kPart;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         int i = 0;
         for (int t = first_tile; t < total; t += stride, ++i) {
             const TileAt at = tiles.at(t);
             const int buf = i & 1;
+            static_assert(kEpiWarps == 8, "two parts");
+            const int part = (at.tokens / 2 + kChunk - 1) / kChunk * kChunk;
+            const int first = (warp - kEpiWarp0) / 4 * part;
             const int m = at.m0 + first;
-            const int count = min(kPart, at.m_end - m);
+            const int count = min(part, at.m_end - m);
             Channel<T> ch;
             ch.n = at.n0 + (warp & 3) * 32 + lane;
             ch.stored = ch.n < a.N;
@@ -688,6 +707,9 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             const uint32_t stage0 = smem_u32(base);
             for (int t = first_tile; t < total && ok; t += stride) {
                 const TileAt at = tiles.at(t);
+                // this CTA's share of the token rows, a box at a time
+                const int m0 = at.m0 + rank * (at.tokens / G);
+                const int boxes = (at.tokens / G + kBox - 1) / kBox;
                 for (int s = 0; s < steps; ++s, ++it, ring.next()) {
                     // (the first pass over the ring finds the phase before the first done)
                     ok = wait_or_abort_m(smem_u32(&sh.empty[ring.at]), ring.phase ^ 1u, abort, a.ctl,
@@ -696,10 +718,14 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                     const uint32_t dst = stage0 + (uint32_t)ring.at * S::kStage;
                     // the leader's barrier counts both CTAs' bytes
                     uint32_t bar = smem_u32(&sh.tma_full[ring.at]);
-                    if (rank == 0) mbar_expect_tx(bar, (uint32_t)(G * (kATile + S::kBTile)));
+                    if (rank == 0) mbar_expect_tx(bar, (uint32_t)(G * (kATile + boxes * kBox * 128)));
                     if (G == 2) bar = leader_addr(bar);
                     tma_load_3d<G>(dst, &map_w, s * 128, at.n0, at.e, bar);
-                    tma_load_3d<G>(dst + kATile, &map_x, s * 128, at.m0 + rank * (TN / G), 0, bar);
+#pragma unroll
+                    for (int i = 0; i < TN / G / kBox; ++i)
+                        if (i < boxes)
+                            tma_load_3d<G>(dst + kATile + i * kBox * 128, &map_x, s * 128,
+                                           m0 + i * kBox, 0, bar);
                 }
             }
             // the last uses of the stages are signalled here before the CTA leaves
@@ -748,7 +774,6 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         // the branch to be one thread, the compiler issues the tensor-core
         // instructions straight from uniform registers.)
         if (elect_one()) {
-            constexpr uint32_t idesc = umma_idesc_scaled(G * kTileN, TN);
             Ring<S::kStages> ring;
             Ring<2> turn, acc;
             const uint32_t stage0 = smem_u32(base), sf0 = smem_u32(sf_base);
@@ -760,6 +785,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)acc.at * TN;
+                const uint32_t idesc = umma_idesc_scaled(G * kTileN, (uint32_t)tiles.at(t).tokens);
                 for (int s = 0; s < steps; s += kTurn, turn.next()) {
                     ok = wait_or_abort_m(smem_u32(&sh.sf_full[turn.at]), turn.phase, abort, a.ctl, 64u,
                                          s);
@@ -881,7 +907,7 @@ nvfp4kv_status launch_tn(const MatmulArgs& a, const void* w_codes, const void* x
                          int sms, cudaStream_t stream) {
     CUtensorMap map_w, map_x;
     if (!make_map(&map_w, w_codes, a.K, a.N, kGrouped ? a.E : 1, kTileN) ||
-        !make_map(&map_x, x_codes, a.K, a.M, 1, TN / G) || !configure<TN, G, kGrouped, kF32>(dev))
+        !make_map(&map_x, x_codes, a.K, a.M, 1, kBox) || !configure<TN, G, kGrouped, kF32>(dev))
         return NVFP4KV_ERR_CUDA;
     const long long n_tiles = (a.N + kTileN * G - 1) / (kTileN * G);
     // grouped: at most one more token tile per expert than the rows fill
@@ -903,6 +929,37 @@ nvfp4kv_status launch_tn(const MatmulArgs& a, const void* w_codes, const void* x
                : NVFP4KV_ERR_CUDA;
 }
 
+// Tokens a tile (TN) for this product.  Wide tiles read each weight for more
+// tokens, and a pair of CTAs shares them (a step of 256 along k took 0.28 us with
+// 32 tokens, 0.30 with 64, 0.38 with 128, 0.48 with a pair's 192 on [7040, 8192]
+// x [2048, 8192]); narrow ones give more CTAs work and leave a shorter epilogue
+// (about 0.8 us and 25 ns a token) after the last MMA: [333, 1056] x [1001, 1056] took 8.7,
+// 9.3, 10.5 and 15 us with them, [880, 2048] x [2048, 2048] 14.3, 10.2, 8.3 and
+// 9.9.  The rule adds these up in ns and takes the least.  A grouped product's
+// group sizes are not known here: its mean stands for all.
+int choose_tile(int M, int N, int K, int E, int sms) {
+    const double steps = (K + kStageK - 1) / kStageK;
+    const int per = (M + E - 1) / E;
+    int best = 0;
+    double least = 0.0;
+    for (const int tn : {192, 128, 64, 32}) {
+        const int g = tn == 192 ? 2 : 1;
+        const int count = (per + tn - 1) / tn;
+        const int size = ((per + count - 1) / count + 15) / 16 * 16;
+        const double tiles = (double)count * E * ((N + kTileN * g - 1) / (kTileN * g));
+        double waves = tiles / (sms / g);
+        if (E == 1 || waves < 1.0) waves = std::ceil(waves);
+        const double sums = steps * (g == 1 ? 250.0 + 1.1 * size : 170.0 + 1.6 * size);
+        const double epilogue = 800.0 + 25.0 * size;
+        const double cost = sums + epilogue + (waves - 1.0) * std::max(sums, epilogue);
+        if (best == 0 || cost < least) {
+            best = tn;
+            least = cost;
+        }
+    }
+    return best;
+}
+
 template <bool kGrouped, bool kF32>
 nvfp4kv_status launch_any(const MatmulArgs& a, const void* w_codes, const void* x_codes,
                           cudaStream_t stream) {
@@ -910,10 +967,12 @@ nvfp4kv_status launch_any(const MatmulArgs& a, const void* w_codes, const void* 
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return NVFP4KV_ERR_CUDA;
     const int sms = sm_count_of(dev);
     if (sms < 2) return NVFP4KV_ERR_CUDA;
-    const int per = kGrouped ? (a.M + a.E - 1) / a.E : a.M;
-    if (per <= 32) return launch_tn<32, 1, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
-    if (per <= 128) return launch_tn<128, 1, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
-    return launch_tn<192, 2, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
+    switch (choose_tile(a.M, a.N, a.K, a.E, sms)) {
+        case 32: return launch_tn<32, 1, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
+        case 64: return launch_tn<64, 1, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
+        case 128: return launch_tn<128, 1, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
+        default: return launch_tn<192, 2, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
+    }
 }
 
 }  // namespace

@@ -273,24 +273,44 @@ def _check_part(t, shape, dtype, name):
                          f"got {t.dtype} {tuple(t.shape)}")
 
 
-class MatrixBuffer:
+class _Parts:
+    """The three device buffers of quantized matrices and their view.  A buffer
+    that is assigned anew is put into the view too."""
+
+    def _set_parts(self, parts, shapes, mode, device):
+        torch = _torch()
+        names = ("codes", "scales", "tensor_scale")
+        dtypes = (torch.uint8, torch.uint8, torch.float32)
+        if parts is None:
+            parts = [torch.zeros(s, dtype=t, device=device) for s, t in zip(shapes, dtypes)]
+        else:
+            for t, s, d, name in zip(parts, shapes, dtypes, names):
+                _check_part(t, s, d, name)
+                if t.device != parts[0].device:
+                    raise ValueError(f"parts on {parts[0].device} and {t.device}")
+        self.view = MatrixView(None, None, None, mode)
+        for name, t in zip(names, parts):
+            setattr(self, name, t)
+
+    def _part(name):
+        def put(self, t):
+            setattr(self, "_" + name, t)
+            setattr(self.view, name, t.data_ptr())
+        return property(lambda self: getattr(self, "_" + name), put)
+
+    codes, scales, tensor_scale = _part("codes"), _part("scales"), _part("tensor_scale")
+    del _part
+
+
+class MatrixBuffer(_Parts):
     """Device buffers of a quantized [M, N] matrix: codes [M, N/2] (uint8),
     scales ([M, N/16] for 1D blocks, [M/16, N/16] for 2D tiles), tensor scale.
     `parts`: a (codes, scales, tensor_scale) that holds one already."""
 
     def __init__(self, M, N, mode, device="cuda", parts=None):
-        import torch
         self.M, self.N, self.mode = M, N, mode
         brows = M if mode == BLOCKS_1D else M // 16
-        shapes = (((M, N // 2), torch.uint8), ((brows, N // 16), torch.uint8),
-                  ((1,), torch.float32))
-        if parts is None:
-            parts = [torch.zeros(shape, dtype=dtype, device=device) for shape, dtype in shapes]
-        else:
-            for t, (shape, dtype), name in zip(parts, shapes, ("codes", "scales",
-                                                               "tensor_scale")):
-                _check_part(t, shape, dtype, name)
-        self.codes, self.scales, self.tensor_scale = parts
+        self._set_parts(parts, ((M, N // 2), (brows, N // 16), (1,)), mode, device)
 
     def to_host(self):
         return dict(codes=self.codes.cpu().numpy(), scales=self.scales.cpu().numpy(),
@@ -315,24 +335,15 @@ def quantize_matrix(X, out: "MatrixBuffer", ws, stream=None):
            "nvfp4kv_quantize_matrix")
 
 
-class GroupedMatrixBuffer:
+class GroupedMatrixBuffer(_Parts):
     """Device buffers of E quantized [M, N] matrices, one after the other:
     codes [E, M, N/2], scales [E, M or M/16, N/16], tensor_scale [E].
     `parts`: a (codes, scales, tensor_scale) that holds them already."""
 
     def __init__(self, E, M, N, mode, device="cuda", parts=None):
-        import torch
         self.E, self.M, self.N, self.mode = E, M, N, mode
         brows = M if mode == BLOCKS_1D else M // 16
-        shapes = (((E, M, N // 2), torch.uint8), ((E, brows, N // 16), torch.uint8),
-                  ((E,), torch.float32))
-        if parts is None:
-            parts = [torch.zeros(shape, dtype=dtype, device=device) for shape, dtype in shapes]
-        else:
-            for t, (shape, dtype), name in zip(parts, shapes, ("codes", "scales",
-                                                               "tensor_scale")):
-                _check_part(t, shape, dtype, name)
-        self.codes, self.scales, self.tensor_scale = parts
+        self._set_parts(parts, ((E, M, N // 2), (E, brows, N // 16), (E,)), mode, device)
 
     def expert(self, e) -> MatrixBuffer:
         """Matrix e, for quantize_matrix to write."""
@@ -341,10 +352,6 @@ class GroupedMatrixBuffer:
 
 
 ACT_NONE, ACT_GELU_TANH, ACT_SILU = 0, 1, 2      # nvfp4kv_activation
-
-
-def _matrix_view(X):
-    return MatrixView(X.codes.data_ptr(), X.scales.data_ptr(), X.tensor_scale.data_ptr(), X.mode)
 
 
 def _row_stride(t, name, M, N):
@@ -361,7 +368,7 @@ def _matmul_args(X, W, Y, ws, bias, activation, gate, gate_rows, rows_per_gate, 
     if X.N != W.N:
         raise ValueError(f"X has {X.N} columns and W {W.N}")
     ep = Epilogue(None, activation, None, rows_per_gate, None, 0)
-    operands = [X.codes, W.codes, ws]
+    operands = [X._codes, W._codes, ws]
     if bias is not None:
         _check_part(bias, lead + (N,), _torch().float32, "bias")
         ep.bias = bias.data_ptr()
@@ -412,9 +419,9 @@ def matmul(X: "MatrixBuffer", W: "MatrixBuffer", Y, ws, bias=None, activation=AC
     gate_rows = -(-X.M // rows_per_gate) if gate is not None else 0
     ep, ldy = _matmul_args(X, W, Y, ws, bias, activation, gate, gate_rows, rows_per_gate,
                            residual, ())
-    xv, wv = _matrix_view(X), _matrix_view(W)
     _check(_on_device_of(Y, stream, lambda s: load().nvfp4kv_matmul(
-        xv, wv, X.M, W.M, X.N, ep, Y.data_ptr(), ldy, _dtype_code(Y), ws.data_ptr(), s)), "nvfp4kv_matmul")
+        X.view, W.view, X.M, W.M, X.N, ep, Y.data_ptr(), ldy, _dtype_code(Y), ws.data_ptr(),
+        s)), "nvfp4kv_matmul")
 
 
 def grouped_matmul(X: "MatrixBuffer", W: "GroupedMatrixBuffer", offsets, Y, ws, bias=None,
@@ -426,10 +433,9 @@ def grouped_matmul(X: "MatrixBuffer", W: "GroupedMatrixBuffer", offsets, Y, ws, 
     if offsets.device != Y.device:
         raise ValueError(f"operands on {offsets.device} and {Y.device}")
     ep, ldy = _matmul_args(X, W, Y, ws, bias, activation, gate, W.E, 0, residual, (W.E,))
-    xv, wv = _matrix_view(X), _matrix_view(W)
     _check(_on_device_of(Y, stream, lambda s: load().nvfp4kv_grouped_matmul(
-        xv, wv, W.E, X.M, W.M, X.N, offsets.data_ptr(), ep, Y.data_ptr(), ldy, _dtype_code(Y),
-        ws.data_ptr(), s)), "nvfp4kv_grouped_matmul")
+        X.view, W.view, W.E, X.M, W.M, X.N, offsets.data_ptr(), ep, Y.data_ptr(), ldy,
+        _dtype_code(Y), ws.data_ptr(), s)), "nvfp4kv_grouped_matmul")
 
 
 def attention_launches(n_chunks, T_c, H, T_q, d=HEAD_DIM) -> int:

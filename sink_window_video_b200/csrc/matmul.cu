@@ -935,23 +935,26 @@ nvfp4kv_status launch_tn(const MatmulArgs& a, const void* w_codes, const void* x
 // x [2048, 8192]); narrow ones give more CTAs work and leave a shorter epilogue
 // (about 0.8 us and 25 ns a token) after the last MMA: [333, 1056] x [1001, 1056] took 8.7,
 // 9.3, 10.5 and 15 us with them, [880, 2048] x [2048, 2048] 14.3, 10.2, 8.3 and
-// 9.9.  The rule adds these up in ns and takes the least.  A grouped product's
-// group sizes are not known here: its mean stands for all.
+// 9.9; a cluster launch costs 1.2 us (one row: 5.4 us with 64 tokens, 6.7 with a
+// pair).  The rule adds these up in ns and takes the least.  A grouped product's
+// group sizes are not known here: their mean stands for all.
 int choose_tile(int M, int N, int K, int E, int sms) {
     const double steps = (K + kStageK - 1) / kStageK;
-    const int per = (M + E - 1) / E;
     int best = 0;
     double least = 0.0;
-    for (const int tn : {192, 128, 64, 32}) {
+    for (const int tn : {32, 64, 128, 192}) {
         const int g = tn == 192 ? 2 : 1;
-        const int count = (per + tn - 1) / tn;
-        const int size = ((per + count - 1) / count + 15) / 16 * 16;
-        const double tiles = (double)count * E * ((N + kTileN * g - 1) / (kTileN * g));
+        const double per = (double)M / E;
+        // groups of all sizes: half a tile each goes to the ragged end
+        const double count = E == 1 ? std::ceil(per / tn) : std::max(1.0, per / tn + 0.5);
+        const double size = std::ceil(per / count / 16.0) * 16.0;
+        const double tiles = count * E * ((N + kTileN * g - 1) / (kTileN * g));
         double waves = tiles / (sms / g);
         if (E == 1 || waves < 1.0) waves = std::ceil(waves);
         const double sums = steps * (g == 1 ? 250.0 + 1.1 * size : 170.0 + 1.6 * size);
         const double epilogue = 800.0 + 25.0 * size;
-        const double cost = sums + epilogue + (waves - 1.0) * std::max(sums, epilogue);
+        const double cost = (g == 1 ? 0.0 : 1200.0) + sums + epilogue +
+                            (waves - 1.0) * std::max(sums, epilogue);
         if (best == 0 || cost < least) {
             best = tn;
             least = cost;

@@ -363,8 +363,8 @@ def _row_stride(t, name, M, N):
 
 
 def _matmul_args(X, W, Y, ws, bias, activation, gate, gate_rows, rows_per_gate, residual, lead):
-    """Checks that the products share; the epilogue and Y's row stride."""
-    M, N = X.M, W.M
+    """Checks that the products share; the epilogue, Y's row stride and dtype."""
+    M, N, y_dtype = X.M, W.M, _dtype_code(Y)
     if X.N != W.N:
         raise ValueError(f"X has {X.N} columns and W {W.N}")
     ep = Epilogue(None, activation, None, rows_per_gate, None, 0)
@@ -387,7 +387,7 @@ def _matmul_args(X, W, Y, ws, bias, activation, gate, gate_rows, rows_per_gate, 
     for t in operands:
         if t.get_device() != device:
             raise ValueError(f"operands on {t.device} and {Y.device}")
-    return ep, _row_stride(Y, "Y", M, N)
+    return ep, _row_stride(Y, "Y", M, N), y_dtype
 
 
 def _on_device_of(Y, stream, call):
@@ -414,14 +414,16 @@ def matmul(X: "MatrixBuffer", W: "MatrixBuffer", Y, ws, bias=None, activation=AC
     W [N, K] into Y [M, N] (float32 or bf16, contiguous rows, any row stride).
     bias [N] float32; gate [ceil(M / rows_per_gate), N] float32, row m takes
     gate row m // rows_per_gate; residual [M, N] of Y's dtype (may be Y)."""
+    if not isinstance(W, MatrixBuffer):
+        raise TypeError(f"W is a {type(W).__name__}, not a MatrixBuffer")
     if gate is not None and rows_per_gate < 1:
         raise ValueError(f"rows_per_gate {rows_per_gate} with a gate")
     gate_rows = -(-X.M // rows_per_gate) if gate is not None else 0
-    ep, ldy = _matmul_args(X, W, Y, ws, bias, activation, gate, gate_rows, rows_per_gate,
-                           residual, ())
+    ep, ldy, y_dtype = _matmul_args(X, W, Y, ws, bias, activation, gate, gate_rows, rows_per_gate,
+                                    residual, ())
     _check(_on_device_of(Y, stream, lambda s: load().nvfp4kv_matmul(
-        X.view, W.view, X.M, W.M, X.N, ep, Y.data_ptr(), ldy, _dtype_code(Y), ws.data_ptr(),
-        s)), "nvfp4kv_matmul")
+        X.view, W.view, X.M, W.M, X.N, ep, Y.data_ptr(), ldy, y_dtype, ws.data_ptr(), s)),
+        "nvfp4kv_matmul")
 
 
 def grouped_matmul(X: "MatrixBuffer", W: "GroupedMatrixBuffer", offsets, Y, ws, bias=None,
@@ -429,13 +431,16 @@ def grouped_matmul(X: "MatrixBuffer", W: "GroupedMatrixBuffer", offsets, Y, ws, 
     """matmul by groups of rows: rows offsets[e] .. offsets[e + 1] - 1 of X
     times matrix e of W; rows outside the groups of Y are left as they are.
     offsets: int32 [E + 1] on the device; bias and gate [E, N] float32."""
+    if not isinstance(W, GroupedMatrixBuffer):
+        raise TypeError(f"W is a {type(W).__name__}, not a GroupedMatrixBuffer")
     _check_part(offsets, (W.E + 1,), _torch().int32, "offsets")
     if offsets.device != Y.device:
         raise ValueError(f"operands on {offsets.device} and {Y.device}")
-    ep, ldy = _matmul_args(X, W, Y, ws, bias, activation, gate, W.E, 0, residual, (W.E,))
+    ep, ldy, y_dtype = _matmul_args(X, W, Y, ws, bias, activation, gate, W.E, 0, residual,
+                                    (W.E,))
     _check(_on_device_of(Y, stream, lambda s: load().nvfp4kv_grouped_matmul(
         X.view, W.view, W.E, X.M, W.M, X.N, offsets.data_ptr(), ep, Y.data_ptr(), ldy,
-        _dtype_code(Y), ws.data_ptr(), s)), "nvfp4kv_grouped_matmul")
+        y_dtype, ws.data_ptr(), s)), "nvfp4kv_grouped_matmul")
 
 
 def attention_launches(n_chunks, T_c, H, T_q, d=HEAD_DIM) -> int:

@@ -543,11 +543,13 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             int cnt = 0;
             if (e < a.E) {
                 const int o0 = a.offsets[e], o1 = a.offsets[e + 1];
-                bad |= o0 < 0 || o1 < o0 || o1 > a.M;
+                const bool fits = o0 >= 0 && o1 >= o0 && o1 <= a.M;
+                const int rows = fits ? o1 - o0 : 0;
+                bad |= !fits;
                 s_off[e] = o0;
                 if (e == a.E - 1) s_off[a.E] = o1;
-                cnt = ((o1 - o0 + TN - 1) / TN) * nt;
-                s_size[e] = o1 > o0 ? tile_rows<TN>(o1 - o0) : 0;
+                cnt = (rows + TN - 1) / TN * nt;
+                s_size[e] = rows > 0 ? tile_rows<TN>(rows) : 0;
             }
             int inc = cnt;
 #pragma unroll

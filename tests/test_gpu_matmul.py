@@ -165,3 +165,250 @@ def test_grouped_many_experts(lib, w_tiles):
     sizes = rng.integers(0, 4, 1024) * (rng.random(1024) < 0.3)
     offsets = [0] + np.cumsum(sizes).tolist()
     Case(lib, 90, offsets[-1] + 1, 48, 64, offsets=offsets, w_tiles=w_tiles).run().check()
+
+
+# ------------------------------------------------------------------ how calls are made
+
+def test_every_tile_width(lib):
+    """Sizes at which the cost rule takes each tile width, the widest (a pair of
+    CTAs) among them, with rows that end inside tiles."""
+    for M, N, K in ((20, 512, 512), (400, 2048, 96), (880, 2048, 2048), (1900, 4100, 544)):
+        Case(lib, M + N, M, N, K, w_tiles=False, residual=True, rpg=150, act="gelu",
+             pad=4).run().check(f"{M}x{N}x{K}")
+
+
+@pytest.mark.parametrize("bf16", [True, False], ids=["bf16", "f32"])
+def test_wide_grouped(lib, bf16):
+    """Groups of several wide tiles beside empty and one-row groups."""
+    offsets = [7, 7, 400, 401, 1201, 1201, 1590]
+    Case(lib, 91, 1600, 2064, 2080, offsets=offsets, bf16=bf16, act="gelu", rpg=1,
+         residual=True).run().check(str(offsets))
+
+
+@pytest.mark.parametrize("rpg", [1, 15, 16, 17, 100])
+def test_gate_stretches(lib, rpg):
+    Case(lib, 92, 333, 144, 128, rpg=rpg, residual=rpg != 16, bf16=rpg % 2 == 0).run().check(str(rpg))
+
+
+def test_unaligned_rows(lib):
+    """Y and the residual at element alignment only, an odd row stride."""
+    import torch
+    for bf16 in (True, False):
+        c = Case(lib, 93, 50, 33, 64, w_tiles=False, bf16=bf16, pad=6)
+        c.Y = c.guard.t[:, 1:34]
+        keep = c.guard.t.clone()
+        r = torch.randn(50, 71, device="cuda").to(c.Y.dtype)
+        c.R = r[:, 3:36]
+        c.r64 = c.R.float().cpu().numpy().astype(np.float64)
+        c.run()
+        torch.cuda.synchronize()
+        c.guard.assert_intact()
+        assert torch.equal(c.guard.t[:, :1].view(torch.uint8), keep[:, :1].view(torch.uint8))
+        assert torch.equal(c.guard.t[:, 34:].view(torch.uint8), keep[:, 34:].view(torch.uint8))
+        y, mag = ref.reference(ref.decode(c.x), ref.decode(c.w), c.bias, "none", None, c.r64)
+        _assert_close(c.Y.float().cpu().numpy().astype(np.float64), y, mag, 64, bf16, "unaligned")
+
+
+def test_rows_far_apart(lib):
+    """A row stride beyond 2^31 bytes."""
+    import torch
+    c = Case(lib, 94, 3, 64, 96, bf16=True)
+    big = torch.empty(2 * ((1 << 30) + 8) + 64, dtype=torch.bfloat16, device="cuda")
+    c.Y = big.as_strided((3, 64), ((1 << 30) + 8, 1))
+    c.run()
+    torch.cuda.synchronize()
+    y, mag = ref.reference(ref.decode(c.x), ref.decode(c.w), c.bias, "none", None, None)
+    _assert_close(c.Y.float().cpu().numpy().astype(np.float64), y, mag, 96, True, "far rows")
+
+
+def test_infinities_and_nan_stay_in_their_places(lib):
+    """Residual and gate values that are not finite reach their own outputs only;
+    those behind the last group are not read into anything."""
+    import torch
+    c = Case(lib, 95, 40, 80, 64, bf16=False, residual=True, offsets=[0, 17, 30], rpg=1)
+    c.R[3, 5], c.R[29, 79], c.R[35, 1] = float("inf"), float("nan"), float("nan")
+    c.dev["gate"][1, 7] = float("-inf")
+    c.run()
+    torch.cuda.synchronize()
+    got = c.Y[:30]
+    bad = torch.zeros(30, 80, dtype=torch.bool)
+    bad[3, 5] = bad[29, 79] = True
+    bad[17:30, 7] = True
+    assert torch.equal(~torch.isfinite(got).cpu(), bad)
+    assert got[3, 5] == float("inf") and torch.isnan(got[29, 79])
+
+
+def test_large_activations_inputs(lib):
+    """Sums far outside the activations' curved range: SiLU and GELU go to the
+    identity and to zero, without a NaN."""
+    import torch
+    for act in ("silu", "gelu"):
+        c = Case(lib, 96, 30, 64, 64, bf16=False, act=act, bias=False)
+        c.x["s"][0] = 1e6
+        c.X.tensor_scale.fill_(1e6)
+        c.run()
+        torch.cuda.synchronize()
+        z, mag = ref.reference(ref.decode(c.x), ref.decode(c.w), None, "none", None, None)
+        got = c.Y.cpu().numpy().astype(np.float64)
+        far = np.abs(z) > 100
+        assert far.mean() > 0.5 and np.isfinite(got).all()
+        want = np.where(z > 0, z, 0.0)
+        tol = mag * (64 / 16 + 32) * 2.0 ** -23
+        assert (np.abs(got - want)[far] <= tol[far]).all()
+
+
+def test_repeated_calls_are_bit_identical(lib):
+    import torch
+    for kw in (dict(M=33, N=272, K=4096), dict(M=1900, N=4112, K=512),
+               dict(M=300, N=272, K=512, offsets=[0, 100, 100, 290])):
+        c = Case(lib, 97, act="gelu", residual=True, **kw).run()
+        torch.cuda.synchronize()
+        first = c.Y.clone()
+        c.Y.zero_()
+        c.run()
+        torch.cuda.synchronize()
+        a, b = (first, c.Y) if c.E is None else (first[:290], c.Y[:290])
+        assert torch.equal(a, b)
+
+
+def test_streams_and_graphs(lib):
+    """A call on another stream than the operands', two captured graphs that
+    share a workspace, replayed on new contents of the same buffers."""
+    import torch
+    c = Case(lib, 98, 70, 144, 256, act="silu", residual=True)
+    d = Case(lib, 99, 90, 272, 160, offsets=[0, 40, 90], bf16=False)
+    d.ws = c.ws
+    d.run()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    c.run(stream=s)
+    s.synchronize()
+    c.check("other stream")
+    graphs = []
+    for k in (c, d):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            k.run()
+        graphs.append(g)
+    rng = np.random.default_rng(5)
+    c.x = ref.random_matrix(rng, (), 70, 256, False)
+    c.X.codes.copy_(torch.from_numpy(c.x["codes"]))
+    c.X.scales.copy_(torch.from_numpy(c.x["scales"]))
+    c.X.tensor_scale.copy_(torch.from_numpy(c.x["s"]))
+    d.offsets = [5, 60, 81]
+    d.off.copy_(torch.tensor(d.offsets, dtype=torch.int32))
+    d.guard.t.copy_(d.before)
+    for g in graphs + graphs:
+        g.replay()
+    c.check("graph")
+    d.check("grouped graph with new offsets")
+    del graphs
+
+
+@pytest.mark.parametrize("offsets", [[0, 5, 3, 9], [-1, 2, 3, 9], [0, 2, 3, 41], [4, 3, 2, 1],
+                                     [0, 1 << 30, 1 << 30, 1 << 30], [0, 0, 0, -(1 << 31)]])
+def test_bad_offsets_are_reported_and_nothing_is_written(lib, offsets):
+    import torch
+    c = Case(lib, 100, 40, 64, 64, offsets=[0, 0, 0, 40])
+    c.off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    c.run()
+    torch.cuda.synchronize()
+    assert lib.workspace_status(c.ws) == lib.ERR_INVALID_ARG
+    assert lib.workspace_status(c.ws) == lib.OK
+    assert torch.equal(c.guard.t.view(torch.uint8), c.before.view(torch.uint8))
+    c.guard.assert_intact()
+    c.off = torch.tensor(c.offsets, dtype=torch.int32, device="cuda")
+    c.run().check("after bad offsets")
+
+
+@pytest.mark.parametrize("M,N", [(20, 256), (1900, 4096)], ids=["one-cta", "pair"])
+def test_wait_timeout_is_reported_and_recoverable(lib, M, N):
+    """A test word in the workspace makes one scale warp withhold its first
+    arrival, so that the waits behind it run out of time: the call must report
+    ERR_DEVICE_TIMEOUT and leave the context, and then the workspace, usable."""
+    import time
+
+    import torch
+    c = Case(lib, 101, M, N, 512)
+    torch.cuda.synchronize()
+    c.ws.view(torch.int32)[7] = 1              # test_flags
+    t0 = time.monotonic()
+    c.run()
+    diag = c.ws.view(torch.int32)[3:7].cpu().numpy()
+    assert lib.workspace_status(c.ws) == lib.ERR_DEVICE_TIMEOUT
+    assert time.monotonic() - t0 < 10
+    assert 60 <= diag[0] <= 67
+    lib.workspace_init(c.ws)
+    c.run().check("after the timeout")
+
+
+def test_a_block_of_the_framework(lib):
+    """The products as a transformer block over the cache uses them: the
+    chunk's activations quantized, projected to queries, keys and values in
+    column ranges of one buffer, keys rotated into the cache, attention over
+    it, the output projected onto the residual stream under a gate for each
+    frame, then text and video rows through their own weights.  Each product is
+    checked against float64 on what it was given."""
+    import torch
+    T, H, d, C = 96, 2, 128, 256
+    rng = np.random.default_rng(8)
+    f = np.float32
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+
+    def rand(*shape, scale=1.0):
+        return (torch.randn(*shape, generator=g, device="cuda") * scale).bfloat16()
+    ws = lib.new_matrix_workspace()
+
+    def quantized(t, mode):
+        q = lib.MatrixBuffer(t.shape[0], t.shape[1], mode)
+        lib.quantize_matrix(t.contiguous(), q, ws)
+        torch.cuda.synchronize()
+        h = q.to_host()
+        return q, dict(codes=h["codes"], scales=h["scales"], s=np.array([h["s"]], f),
+                       tiles=mode == lib.TILES_2D)
+
+    def checked(Y, x, w, bias, act, gate, res, K, what):
+        y, mag = ref.reference(ref.decode(x), ref.decode(w), bias, act, gate, res)
+        _assert_close(Y.float().cpu().numpy().astype(np.float64), y, mag, K,
+                      Y.dtype == torch.bfloat16, what)
+
+    x = rand(T, C)
+    Wq, wq = quantized(rand(3 * H * d, C, scale=C ** -0.5), lib.TILES_2D)
+    Wo, wo = quantized(rand(C, H * d, scale=(H * d) ** -0.5), lib.TILES_2D)
+    X, xh = quantized(x, lib.BLOCKS_1D)
+    bias = rng.standard_normal(3 * H * d).astype(f)
+    qkv = torch.empty(T, 3 * H * d, dtype=torch.bfloat16, device="cuda")
+    lib.matmul(X, Wq, qkv, ws, bias=_cuda(bias))
+    checked(qkv, xh, wq, bias, "none", None, None, C, "projection")
+
+    q, k, v = (qkv[:, i * H * d:(i + 1) * H * d].contiguous().view(T, H, d) for i in range(3))
+    cache = lib.KVCache(1, H, T, 1, 0, 1)
+    table = lib.RopeTable(3, 4, 8).fill(0)
+    cache.append_rope(0, k, v, table)
+    O = torch.empty(T, H, d, dtype=torch.bfloat16, device="cuda")
+    cache.attention(0, lib.rope(q, table), O)
+
+    A, ah = quantized(O.view(T, H * d), lib.BLOCKS_1D)
+    gate = rng.standard_normal((3, C)).astype(f)
+    stream = x.clone()
+    lib.matmul(A, Wo, stream, ws, gate=_cuda(gate), rows_per_gate=32, residual=stream)
+    checked(stream, ah, wo, None, "none", gate[np.arange(T) // 32],
+            x.float().cpu().numpy().astype(np.float64), H * d, "output projection")
+
+    Wg = lib.GroupedMatrixBuffer(2, 128, C, lib.TILES_2D)
+    hosts = []
+    for e in range(2):
+        m = Wg.expert(e)
+        lib.quantize_matrix(rand(128, C, scale=C ** -0.5), m, ws)
+        torch.cuda.synchronize()
+        h = m.to_host()
+        hosts.append(dict(codes=h["codes"], scales=h["scales"], s=np.array([h["s"]], f), tiles=True))
+    S, sh = quantized(stream, lib.BLOCKS_1D)
+    up = torch.empty(T, 128, device="cuda")
+    lib.grouped_matmul(S, Wg, _cuda(np.array([0, 20, T], np.int32)), up, ws,
+                       activation=lib.ACT_GELU_TANH)
+    for e, (a, b) in enumerate(((0, 20), (20, T))):
+        part = dict(sh, codes=sh["codes"][a:b], scales=sh["scales"][a:b])
+        checked(up[a:b], part, hosts[e], None, "gelu", None, None, C, f"group {e}")
+    assert lib.workspace_status(ws) == lib.OK and cache.check_status() == lib.OK

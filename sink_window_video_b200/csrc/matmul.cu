@@ -55,6 +55,8 @@ constexpr int kATile = kTileN * 128;        // bytes of codes of a weight tile's
 constexpr int kTurn = 4;
 constexpr int kSfBlock = 512 + 16;
 constexpr int kSfGroup = 4 * kTurn * kSfBlock;
+constexpr int kChunk = 16;                  // tokens an epilogue warp takes at a time
+constexpr int kEpiBytes = kChunk * 32 * 2;  // its staging of bf16 rows
 constexpr int kMaxStages = 12;
 constexpr unsigned long long kLandNs = 10ull * 1000 * 1000;   // 10 ms
 constexpr size_t kStageRoom = 216 * 1024;    // of 227 KB; the rest: offsets, barriers, alignment
@@ -86,9 +88,10 @@ struct Shape {
     static constexpr int kStage = kATile + kBTile;
     static constexpr int kGroups = 1 + (TN + 127) / 128;     // 128-row groups of scales
     static constexpr int kSfStage = kGroups * kSfGroup;
-    static constexpr int kFit = (int)((kStageRoom - 2 * kSfStage) / kStage);
+    static constexpr int kFit = (int)((kStageRoom - 2 * kSfStage - kEpiWarps * kEpiBytes) / kStage);
     static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
-    static constexpr size_t kSmem = (size_t)kStages * kStage + 2 * kSfStage + 1024;
+    static constexpr size_t kSmem = (size_t)kStages * kStage + 2 * kSfStage + kEpiWarps * kEpiBytes +
+                                    1024;
     static_assert(kStage % 1024 == 0, "stages keep the swizzle alignment");
     static constexpr uint32_t kColSFA = 2 * TN, kColSFB = 2 * TN + 16;   // 16 and up to 32 columns
     static_assert(2 * TN + 16 + 8 * 4 <= kColsMM, "two accumulators beside the scales");
@@ -316,8 +319,6 @@ struct Channel {
     const T* r;
 };
 
-constexpr int kChunk = 16;      // tokens an epilogue warp takes at a time
-
 // The residual of the next C tokens, `count` of which exist.
 template <int C, class T>
 __device__ __forceinline__ void load_residual(const MatmulArgs& a, Walk<const T>& r, T* res, int count) {
@@ -374,6 +375,149 @@ __device__ __forceinline__ void epilogue_run(const MatmulArgs& a, uint32_t taddr
         }
         tmem_wait_ld();
         finish_tokens<kChunk, kAct, kRes, false>(a, v, res, ch, y, count + here, &ch.gate);
+    }
+}
+
+// A bf16 tile's rows in 16-byte pieces (8 channels of one token).  The sums are
+// read from tensor memory in the layout of 8 x 8 matrix fragments (thread t of a
+// warp: channel t / 4, tokens 2 (t % 4) and the next), so that a pair of tokens
+// packs into one register and stmatrix.trans turns fragments into rows of
+// channels: per 16 tokens 2 stores of 16 bytes a thread in place of 16 of 2 bytes.
+// The residual comes the other way, through ldmatrix.trans.
+struct Pieces {
+    int n0, lane;            // the warp's first channel
+    uint32_t stage;          // its 1 KB of shared memory: 16 tokens x 32 channels
+    float bias[4], gate[4];  // of channels n0 + 8 i + lane / 4
+    bool here;               // this thread's piece (channels n0 + 8 (lane % 4) ..) exists
+
+    // byte offset of piece p of token t; the swizzle spreads both the 8 tokens of
+    // one piece and the 4 pieces of two tokens over all banks
+    __device__ __forceinline__ static uint32_t at(int t, int p) {
+        return (uint32_t)(t * 64 + ((p ^ (t >> 1)) & 3) * 16);
+    }
+};
+
+__device__ __forceinline__ void tmem_ld_frag2(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void stmatrix4_trans(uint32_t addr, const uint32_t* r) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t addr, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// `count` tokens from row m on under pc.gate, accumulators in tensor memory at
+// taddr.
+template <int kAct, bool kRes>
+__device__ __forceinline__ void epilogue_pieces(const MatmulArgs& a, uint32_t taddr, const Pieces& pc,
+                                                int m, int count, float alpha) {
+    const int tok = pc.lane >> 2, piece = pc.lane & 3;
+    const size_t first = (size_t)(m + tok), col = (size_t)(pc.n0 + 8 * piece);
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.Y) + first * a.ldy + col;
+    const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(a.residual) + first * a.ldr + col;
+    // the rows that this thread hands to stmatrix / ldmatrix (matrix lane / 8 =
+    // channels 8 (lane / 8) .., token lane % 8), and its own pieces
+    const uint32_t frag = pc.stage + Pieces::at(pc.lane & 7, pc.lane >> 3);
+    const uint32_t own = pc.stage + Pieces::at(tok, piece);
+    constexpr uint32_t kHalf = 8 * 64;       // tokens 8 .. 15 (the swizzle repeats)
+    uint4 next[2];
+    auto load = [&](int left) {
+        next[0] = next[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (pc.here && tok < left) next[0] = *reinterpret_cast<const uint4*>(r);
+        if (pc.here && tok + 8 < left) next[1] = *reinterpret_cast<const uint4*>(r + 8 * a.ldr);
+        r += kChunk * a.ldr;
+    };
+    if (kRes) load(count);
+#pragma unroll 1
+    for (; count > 0; count -= kChunk, taddr += kChunk) {
+        uint32_t v[16], res[8];
+        tmem_ld_frag2(taddr, v);
+        tmem_ld_frag2(taddr + (16u << 16), v + 8);
+        __syncwarp();                        // the last chunk's pieces are read
+        if (kRes) {
+            sts16(own, next[0]);
+            sts16(own + kHalf, next[1]);
+            load(count - kChunk);
+            __syncwarp();
+            ldmatrix4_trans(frag, res);
+            ldmatrix4_trans(frag + kHalf, res + 4);
+            __syncwarp();
+        }
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {        // tokens 8 j ..
+            uint32_t p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {    // channels 8 i ..
+                const uint32_t* s = v + 8 * (i >> 1) + 4 * j + 2 * (i & 1);
+                float2 z = __ffma2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])),
+                                      make_float2(alpha, alpha),
+                                      make_float2(pc.bias[i], pc.bias[i]));
+                z = act_pair<kAct>(z);
+                const float2 g = make_float2(pc.gate[i], pc.gate[i]);
+                if (kRes) {
+                    const uint32_t w = res[4 * j + i];
+                    z = __ffma2_rn(z, g, make_float2(__uint_as_float(w << 16),
+                                                     __uint_as_float(w & 0xFFFF0000u)));
+                } else {
+                    z = __fmul2_rn(z, g);
+                }
+                const __nv_bfloat162 h = __floats2bfloat162_rn(z.x, z.y);
+                p[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            stmatrix4_trans(frag + j * kHalf, p);
+        }
+        __syncwarp();
+        if (pc.here && tok < count) *reinterpret_cast<uint4*>(y) = lds16(own);
+        if (pc.here && tok + 8 < count) *reinterpret_cast<uint4*>(y + 8 * a.ldy) = lds16(own + kHalf);
+        y += kChunk * a.ldy;
+    }
+}
+
+// One warp's share of a bf16 tile in pieces: stretches of tokens under one gate.
+template <int kAct, bool kGrouped>
+__device__ __forceinline__ void epilogue_pieces_share(const MatmulArgs& a, uint32_t taddr, Pieces& pc,
+                                                      int m, int count, float alpha) {
+    const bool by_row = !kGrouped && a.gate;
+#pragma unroll 1
+    while (count > 0) {
+        int n = count;
+        if (by_row) {
+            const int row = m / a.rows_per_gate;
+            n = (int)min((long long)count, (long long)(row + 1) * a.rows_per_gate - m);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = pc.n0 + 8 * i + (pc.lane >> 2);
+                pc.gate[i] = c < a.N ? __ldg(a.gate + (size_t)row * a.N + c) : 0.0f;
+            }
+        }
+        if (a.residual) epilogue_pieces<kAct, true>(a, taddr, pc, m, n, alpha);
+        else epilogue_pieces<kAct, false>(a, taddr, pc, m, n, alpha);
+        taddr += n;
+        m += n;
+        count -= n;
     }
 }
 
@@ -580,6 +724,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     const int turns = (steps + kTurn - 1) / kTurn;
     const int kbytes = a.K / 16;
     uint8_t* sf_base = base + (size_t)S::kStages * S::kStage;
+    uint8_t* epi_base = sf_base + 2 * S::kSfStage;
 
     if (warp < kEpiWarp0)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
@@ -667,6 +812,13 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         // warp = lane quarter (warp % 4) of one part of the tile's tokens
         using T = typename OutType<kF32>::T;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        // bf16 rows go in 16-byte pieces where every piece is whole and aligned
+        // and a gate holds for at least a chunk
+        const uintptr_t align = reinterpret_cast<uintptr_t>(a.Y) | (uintptr_t)(a.ldy * 2) |
+                                reinterpret_cast<uintptr_t>(a.residual) |
+                                (uintptr_t)(a.residual ? a.ldr * 2 : 0);
+        const bool pieces = (align & 15u) == 0 && a.N % 8 == 0 &&
+                            (kGrouped || !a.gate || a.rows_per_gate >= kChunk);
         int i = 0;
         for (int t = first_tile; t < total; t += stride, ++i) {
             const TileAt at = tiles.at(t);
@@ -690,7 +842,24 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             if (!__all_sync(0xFFFFFFFFu, got)) break;
             tc_fence_after();
             const uint32_t ta = tmem + lane_base + (uint32_t)(buf * TN + first);
-            if (a.act == NVFP4KV_ACT_GELU_TANH)
+            if (!kF32 && pieces) {
+                Pieces pc;
+                pc.n0 = ch.n - lane;
+                pc.lane = lane;
+                pc.stage = smem_u32(epi_base) + (uint32_t)(warp - kEpiWarp0) * kEpiBytes;
+                pc.here = pc.n0 + 8 * (lane & 3) < a.N;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    pc.bias[i] = __shfl_sync(0xFFFFFFFFu, ch.bias, 8 * i + (lane >> 2));
+                    pc.gate[i] = __shfl_sync(0xFFFFFFFFu, ch.gate, 8 * i + (lane >> 2));
+                }
+                if (a.act == NVFP4KV_ACT_GELU_TANH)
+                    epilogue_pieces_share<NVFP4KV_ACT_GELU_TANH, kGrouped>(a, ta, pc, m, count, ch.alpha);
+                else if (a.act == NVFP4KV_ACT_SILU)
+                    epilogue_pieces_share<NVFP4KV_ACT_SILU, kGrouped>(a, ta, pc, m, count, ch.alpha);
+                else
+                    epilogue_pieces_share<NVFP4KV_ACT_NONE, kGrouped>(a, ta, pc, m, count, ch.alpha);
+            } else if (a.act == NVFP4KV_ACT_GELU_TANH)
                 epilogue_share<NVFP4KV_ACT_GELU_TANH, kGrouped>(a, ta, m, count, ch);
             else if (a.act == NVFP4KV_ACT_SILU)
                 epilogue_share<NVFP4KV_ACT_SILU, kGrouped>(a, ta, m, count, ch);

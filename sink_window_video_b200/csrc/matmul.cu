@@ -56,7 +56,7 @@ constexpr int kTurn = 4;
 constexpr int kSfBlock = 512 + 16;
 constexpr int kSfGroup = 4 * kTurn * kSfBlock;
 constexpr int kChunk = 16;                  // tokens an epilogue warp takes at a time
-constexpr int kEpiBytes = kChunk * 32 * 2;  // its staging of bf16 rows
+constexpr int kEpiBytes = 1024;             // its staging: 16 bf16 or 8 fp32 rows of 32
 constexpr int kMaxStages = 12;
 constexpr unsigned long long kLandNs = 10ull * 1000 * 1000;   // 10 ms
 constexpr size_t kStageRoom = 216 * 1024;    // of 227 KB; the rest: offsets, barriers, alignment
@@ -68,6 +68,11 @@ constexpr size_t kStageRoom = 216 * 1024;    // of 227 KB; the rest: offsets, ba
 __host__ __device__ constexpr uint32_t umma_idesc_scaled(uint32_t m, uint32_t n) {
     return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
+
+template <int V>
+struct IntC {
+    static constexpr int value = V;
+};
 
 // Position in a ring of N slots and the parity of its current pass.
 template <int N>
@@ -275,19 +280,6 @@ __device__ __forceinline__ float2 act_pair(float2 z) {
     return __fmul2_rn(z, __fmul2_rn(make_float2(d.y, d.x), make_float2(r, r)));
 }
 
-template <bool kF32>
-struct OutType {
-    using T = float;
-};
-template <>
-struct OutType<false> {
-    using T = __nv_bfloat16;
-};
-__device__ __forceinline__ float load_out(const float* p) { return *p; }
-__device__ __forceinline__ float load_out(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
 // Walks down the rows of one channel.  Four addresses take turns, each stepping
 // four rows, so that a row does not wait for the 64-bit addition of the row
 // before; the empty asm keeps the compiler from forming every multiple of the
@@ -310,30 +302,29 @@ struct Walk {
 
 // What an epilogue thread keeps of its tile: its channel n, that channel's
 // constants, and where the next token's result and residual are.
-template <class T>
 struct Channel {
     int n;
     bool stored;             // n < N
     float alpha, bias, gate;
-    T* y;
-    const T* r;
+    float* y;
+    const float* r;
 };
 
 // The residual of the next C tokens, `count` of which exist.
-template <int C, class T>
-__device__ __forceinline__ void load_residual(const MatmulArgs& a, Walk<const T>& r, T* res, int count) {
+template <int C>
+__device__ __forceinline__ void load_residual(const MatmulArgs& a, Walk<const float>& r, float* res, int count) {
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-        const T* p = r.row(j, a.ldr);
+        const float* p = r.row(j, a.ldr);
         if (j < count) res[j] = *p;
     }
 }
 
 // The next C tokens of one channel, `count` of which exist, from their sums v and
 // residual res; the gates are g[0 .. C) where kGates, else g[0].
-template <int C, int kAct, bool kRes, bool kGates, class T>
-__device__ __forceinline__ void finish_tokens(const MatmulArgs& a, const uint32_t* v, const T* res,
-                                              const Channel<T>& ch, Walk<T>& y, int count,
+template <int C, int kAct, bool kRes, bool kGates>
+__device__ __forceinline__ void finish_tokens(const MatmulArgs& a, const uint32_t* v, const float* res,
+                                              const Channel& ch, Walk<float>& y, int count,
                                               const float* g) {
 #pragma unroll
     for (int j = 0; j < C; j += 2) {
@@ -341,24 +332,24 @@ __device__ __forceinline__ void finish_tokens(const MatmulArgs& a, const uint32_
                               make_float2(ch.alpha, ch.alpha), make_float2(ch.bias, ch.bias));
         z = act_pair<kAct>(z);
         const float2 gg = kGates ? make_float2(g[j], g[j + 1]) : make_float2(g[0], g[0]);
-        if (kRes) z = __ffma2_rn(z, gg, make_float2(load_out(&res[j]), load_out(&res[j + 1])));
+        if (kRes) z = __ffma2_rn(z, gg, make_float2(res[j], res[j + 1]));
         else z = __fmul2_rn(z, gg);
-        T* y0 = y.row(j, a.ldy);
-        T* y1 = y.row(j + 1, a.ldy);
-        if (j < count) store_out(y0, z.x);
-        if (j + 1 < count) store_out(y1, z.y);
+        float* y0 = y.row(j, a.ldy);
+        float* y1 = y.row(j + 1, a.ldy);
+        if (j < count) *y0 = z.x;
+        if (j + 1 < count) *y1 = z.y;
     }
 }
 
 // `count` tokens of one channel, accumulators in tensor memory at taddr, all under
 // ch.gate; the next 16's residual is on its way meanwhile.  Leaves ch.y and ch.r
 // behind the last token.
-template <int kAct, bool kRes, class T>
-__device__ __forceinline__ void epilogue_run(const MatmulArgs& a, uint32_t taddr, Channel<T>& ch,
+template <int kAct, bool kRes>
+__device__ __forceinline__ void epilogue_run(const MatmulArgs& a, uint32_t taddr, Channel& ch,
                                              int count) {
-    T next[kRes ? kChunk : 1];
-    Walk<T> y(ch.y, a.ldy);
-    Walk<const T> r(ch.r, kRes ? a.ldr : 0);
+    float next[kRes ? kChunk : 1];
+    Walk<float> y(ch.y, a.ldy);
+    Walk<const float> r(ch.r, kRes ? a.ldr : 0);
     ch.y += (size_t)count * a.ldy;
     if (kRes) ch.r += (size_t)count * a.ldr;
     const int here = ch.stored ? 0 : -(1 << 20);      // tokens of no stored channel: none
@@ -367,7 +358,7 @@ __device__ __forceinline__ void epilogue_run(const MatmulArgs& a, uint32_t taddr
     for (; count > 0; count -= kChunk, taddr += kChunk) {
         uint32_t v[kChunk];
         tmem_ld16(taddr, v);
-        T res[kRes ? kChunk : 1];
+        float res[kRes ? kChunk : 1];
         if (kRes) {
 #pragma unroll
             for (int j = 0; j < kChunk; ++j) res[j] = next[j];
@@ -375,6 +366,64 @@ __device__ __forceinline__ void epilogue_run(const MatmulArgs& a, uint32_t taddr
         }
         tmem_wait_ld();
         finish_tokens<kChunk, kAct, kRes, false>(a, v, res, ch, y, count + here, &ch.gate);
+    }
+}
+
+// `count` tokens from row m on, their gates looked up one by one.
+template <int kAct>
+__device__ __forceinline__ void epilogue_gates(const MatmulArgs& a, uint32_t taddr, Channel& ch, int m,
+                                               int count) {
+    constexpr int C = 4;
+    Walk<float> y(ch.y, a.ldy);
+    Walk<const float> r(ch.r, a.ldr);
+    int q = m / a.rows_per_gate, rem = m - q * a.rows_per_gate;
+#pragma unroll 1
+    for (; count > 0; count -= C, taddr += C) {
+        const int here = ch.stored ? count : 0;
+        uint32_t v[C];
+        tmem_ld4(taddr, v);
+        float res[C] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (a.residual) load_residual<C>(a, r, res, here);
+        float g[C];
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            if (j < here) g[j] = __ldg(a.gate + (size_t)q * a.N + ch.n);
+            if (++rem == a.rows_per_gate) {
+                rem = 0;
+                ++q;
+            }
+        }
+        tmem_wait_ld();
+        finish_tokens<C, kAct, true, true>(a, v, res, ch, y, here, g);
+        __syncwarp();
+    }
+}
+
+// One warp's share of a tile: `count` tokens from row m on of 32 channels, their
+// sums in tensor memory from taddr on.  Gates of 16 rows or more are taken a
+// stretch of tokens under one gate at a time.
+template <int kAct, bool kGrouped>
+__device__ __forceinline__ void epilogue_share(const MatmulArgs& a, uint32_t taddr, int m, int count,
+                                               Channel ch) {
+    const bool by_row = !kGrouped && a.gate;
+    if (by_row && a.rows_per_gate < kChunk) {
+        epilogue_gates<kAct>(a, taddr, ch, m, count);
+        return;
+    }
+#pragma unroll 1
+    while (count > 0) {
+        int n = count;
+        if (by_row) {
+            const int row = m / a.rows_per_gate;
+            n = (int)min((long long)count, (long long)(row + 1) * a.rows_per_gate - m);
+            if (ch.stored) ch.gate = __ldg(a.gate + (size_t)row * a.N + ch.n);
+        }
+        if (a.residual) epilogue_run<kAct, true>(a, taddr, ch, n);
+        else epilogue_run<kAct, false>(a, taddr, ch, n);
+        __syncwarp();
+        taddr += n;
+        m += n;
+        count -= n;
     }
 }
 
@@ -521,45 +570,109 @@ __device__ __forceinline__ void epilogue_pieces_share(const MatmulArgs& a, uint3
     }
 }
 
-// `count` tokens from row m on, their gates looked up one by one.
-template <int kAct, class T>
-__device__ __forceinline__ void epilogue_gates(const MatmulArgs& a, uint32_t taddr, Channel<T>& ch, int m,
-                                               int count) {
-    constexpr int C = 4;
-    Walk<T> y(ch.y, a.ldy);
-    Walk<const T> r(ch.r, a.ldr);
-    int q = m / a.rows_per_gate, rem = m - q * a.rows_per_gate;
+// A bf16 tile whose rows are no whole pieces, or whose gates change within a
+// chunk, by way of fp32 rows: 8 tokens at a time, sums with a thread a channel
+// (bias, activation and gate there), then through shared memory to a thread for 4
+// channels of one token, which adds the residual, rounds and stores: 8 bytes
+// at once where `vec`, else element by element.
+__device__ __forceinline__ void unpack4(const uint2& v, float* f) {
+    f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint2 pack4(const float* f) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// `count` tokens from row m on, accumulators in tensor memory at taddr.  gate: of
+// this lane's channel n0 + lane; kGates: looked up for each token instead.
+template <int kAct, bool kRes, bool kGates>
+__device__ __forceinline__ void epilogue_rows(const MatmulArgs& a, uint32_t taddr, int n0, int lane,
+                                              float* stage, int m, int count, float alpha, float bias,
+                                              float gate, bool vec) {
+    using T = __nv_bfloat16;
+    constexpr int C = 8;
+    const int tok = lane >> 3, col = 4 * (lane & 7);
+    const int here = min(4, a.N - n0 - col);             // channels of this thread that exist
+    T* y = static_cast<T*>(a.Y) + (size_t)(m + tok) * a.ldy + n0 + col;
+    const T* r = static_cast<const T*>(a.residual) + (size_t)(m + tok) * a.ldr + n0 + col;
+    uint2 next[2];
+    auto load = [&](int left) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (tok + 4 * h < left && here > 0) next[h] = *reinterpret_cast<const uint2*>(r + 4 * h * a.ldr);
+        r += C * a.ldr;
+    };
+    if (kRes && vec) load(count);
 #pragma unroll 1
     for (; count > 0; count -= C, taddr += C) {
-        const int here = ch.stored ? count : 0;
         uint32_t v[C];
-        tmem_ld4(taddr, v);
-        T res[C] = {T(0.0f), T(0.0f), T(0.0f), T(0.0f)};
-        if (a.residual) load_residual<C>(a, r, res, here);
-        float g[C];
+        tmem_ld8(taddr, v);
+        tmem_wait_ld();
+        __syncwarp();                        // the last tokens' rows are read
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
-            if (j < here) g[j] = __ldg(a.gate + (size_t)q * a.N + ch.n);
-            if (++rem == a.rows_per_gate) {
-                rem = 0;
-                ++q;
+        for (int j = 0; j < C; j += 2) {
+            float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+                                  make_float2(alpha, alpha), make_float2(bias, bias));
+            z = __fmul2_rn(act_pair<kAct>(z), make_float2(gate, gate));
+            stage[j * 32 + lane] = z.x;
+            stage[(j + 1) * 32 + lane] = z.y;
+        }
+        __syncwarp();
+        uint2 now[2];
+        if (kRes && vec) {
+            now[0] = next[0];
+            now[1] = next[1];
+            load(count - C);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool mine = tok + 4 * h < count && here > 0;
+            const float4 q = *reinterpret_cast<const float4*>(stage + (tok + 4 * h) * 32 + col);
+            float f[4] = {q.x, q.y, q.z, q.w};
+            if (kGates && mine) {
+                const float* g = a.gate + (size_t)((m + tok + 4 * h) / a.rows_per_gate) * a.N + n0 + col;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < here) f[i] *= __ldg(g + i);
+            }
+            if (vec) {
+                if (kRes) {
+                    float w[4];
+                    unpack4(now[h], w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[i] += w[i];
+                }
+                if (mine) *reinterpret_cast<uint2*>(y + 4 * h * a.ldy) = pack4(f);
+            } else if (mine) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < here) {
+                        if (kRes) f[i] += __bfloat162float(r[4 * h * a.ldr + i]);
+                        y[4 * h * a.ldy + i] = __float2bfloat16_rn(f[i]);
+                    }
             }
         }
-        tmem_wait_ld();
-        finish_tokens<C, kAct, true, true>(a, v, res, ch, y, here, g);
-        __syncwarp();
+        y += C * a.ldy;
+        m += C;
+        if (!vec) r += C * a.ldr;
     }
 }
 
-// One warp's share of a tile: `count` tokens from row m on of 32 channels, their
-// sums in tensor memory from taddr on.  Gates of 16 rows or more are taken a
-// stretch of tokens under one gate at a time.
-template <int kAct, bool kGrouped, class T>
-__device__ __forceinline__ void epilogue_share(const MatmulArgs& a, uint32_t taddr, int m, int count,
-                                               Channel<T> ch) {
+// One warp's share of a tile in fp32 rows: stretches of tokens under one gate, or
+// all of them with a gate looked up for each where a gate holds for less than 16.
+template <int kAct, bool kGrouped>
+__device__ __forceinline__ void epilogue_rows_share(const MatmulArgs& a, uint32_t taddr, int n0, int lane,
+                                                    float* stage, int m, int count, float alpha,
+                                                    float bias, float gate, bool vec) {
     const bool by_row = !kGrouped && a.gate;
     if (by_row && a.rows_per_gate < kChunk) {
-        epilogue_gates<kAct>(a, taddr, ch, m, count);
+        if (a.residual)
+            epilogue_rows<kAct, true, true>(a, taddr, n0, lane, stage, m, count, alpha, bias, 1.0f,
+                                                  vec);
+        else
+            epilogue_rows<kAct, false, true>(a, taddr, n0, lane, stage, m, count, alpha, bias, 1.0f,
+                                                   vec);
         return;
     }
 #pragma unroll 1
@@ -568,11 +681,13 @@ __device__ __forceinline__ void epilogue_share(const MatmulArgs& a, uint32_t tad
         if (by_row) {
             const int row = m / a.rows_per_gate;
             n = (int)min((long long)count, (long long)(row + 1) * a.rows_per_gate - m);
-            if (ch.stored) ch.gate = __ldg(a.gate + (size_t)row * a.N + ch.n);
+            gate = n0 + lane < a.N ? __ldg(a.gate + (size_t)row * a.N + n0 + lane) : 0.0f;
         }
-        if (a.residual) epilogue_run<kAct, true>(a, taddr, ch, n);
-        else epilogue_run<kAct, false>(a, taddr, ch, n);
-        __syncwarp();
+        if (a.residual)
+            epilogue_rows<kAct, true, false>(a, taddr, n0, lane, stage, m, n, alpha, bias, gate, vec);
+        else
+            epilogue_rows<kAct, false, false>(a, taddr, n0, lane, stage, m, n, alpha, bias, gate,
+                                                    vec);
         taddr += n;
         m += n;
         count -= n;
@@ -810,61 +925,69 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     } else if (warp >= kEpiWarp0) {
         // ------------------------------------------------------------ epilogue
         // warp = lane quarter (warp % 4) of one part of the tile's tokens
-        using T = typename OutType<kF32>::T;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        // bf16 rows go in 16-byte pieces where every piece is whole and aligned
-        // and a gate holds for at least a chunk
+        uint8_t* stage = epi_base + (warp - kEpiWarp0) * kEpiBytes;
+        // bf16 rows go in whole pieces of 8 elements where a gate holds for at
+        // least a chunk, else in pieces of 4 or by element
         const uintptr_t align = reinterpret_cast<uintptr_t>(a.Y) | (uintptr_t)(a.ldy * 2) |
-                                reinterpret_cast<uintptr_t>(a.residual) |
-                                (uintptr_t)(a.residual ? a.ldr * 2 : 0);
-        const bool pieces = (align & 15u) == 0 && a.N % 8 == 0 &&
+                                (a.residual ? reinterpret_cast<uintptr_t>(a.residual) |
+                                                  (uintptr_t)(a.ldr * 2)
+                                            : 0);
+        const bool vec = align % 8 == 0 && a.N % 4 == 0;
+        const bool pieces = align % 16 == 0 && a.N % 8 == 0 &&
                             (kGrouped || !a.gate || a.rows_per_gate >= kChunk);
         int i = 0;
         for (int t = first_tile; t < total; t += stride, ++i) {
             const TileAt at = tiles.at(t);
             const int buf = i & 1;
-            static_assert(kEpiWarps == 8, "two parts");
-            const int part = (at.tokens / 2 + kChunk - 1) / kChunk * kChunk;
+            constexpr int kParts = kEpiWarps / 4;
+            const int part = ((at.tokens + kParts - 1) / kParts + kChunk - 1) / kChunk * kChunk;
             const int first = (warp - kEpiWarp0) / 4 * part;
             const int m = at.m0 + first;
             const int count = min(part, at.m_end - m);
-            Channel<T> ch;
-            ch.n = at.n0 + (warp & 3) * 32 + lane;
-            ch.stored = ch.n < a.N;
-            const size_t en = (size_t)at.e * a.N + ch.n;
-            ch.alpha = __ldg(a.x_scale) * __ldg(a.w_scale + at.e);
-            ch.bias = (a.bias && ch.stored) ? __ldg(a.bias + en) : 0.0f;
-            ch.gate = (a.gate && kGrouped && ch.stored) ? __ldg(a.gate + en) : 1.0f;
-            ch.y = static_cast<T*>(a.Y) + (size_t)m * a.ldy + ch.n;
-            ch.r = static_cast<const T*>(a.residual) + (size_t)m * a.ldr + ch.n;
+            const int n0 = at.n0 + (warp & 3) * 32;
+            const bool stored = n0 + lane < a.N;
+            const size_t en = (size_t)at.e * a.N + n0 + lane;
+            const float alpha = __ldg(a.x_scale) * __ldg(a.w_scale + at.e);
+            const float bias = (a.bias && stored) ? __ldg(a.bias + en) : 0.0f;
+            const float gate = (a.gate && kGrouped && stored) ? __ldg(a.gate + en) : 1.0f;
             const bool got = wait_or_abort_m(smem_u32(&sh.acc_full[buf]), (uint32_t)((i >> 1) & 1),
                                              abort, a.ctl, 61u, i);
             if (!__all_sync(0xFFFFFFFFu, got)) break;
             tc_fence_after();
             const uint32_t ta = tmem + lane_base + (uint32_t)(buf * TN + first);
-            if (!kF32 && pieces) {
-                Pieces pc;
-                pc.n0 = ch.n - lane;
-                pc.lane = lane;
-                pc.stage = smem_u32(epi_base) + (uint32_t)(warp - kEpiWarp0) * kEpiBytes;
-                pc.here = pc.n0 + 8 * (lane & 3) < a.N;
+            auto finish = [&](auto act) {
+                constexpr int kAct = decltype(act)::value;
+                if constexpr (kF32) {
+                    Channel ch;
+                    ch.n = n0 + lane;
+                    ch.stored = stored;
+                    ch.alpha = alpha;
+                    ch.bias = bias;
+                    ch.gate = gate;
+                    ch.y = static_cast<float*>(a.Y) + (size_t)m * a.ldy + ch.n;
+                    ch.r = static_cast<const float*>(a.residual) + (size_t)m * a.ldr + ch.n;
+                    epilogue_share<kAct, kGrouped>(a, ta, m, count, ch);
+                } else if (pieces) {
+                    Pieces pc;
+                    pc.n0 = n0;
+                    pc.lane = lane;
+                    pc.stage = smem_u32(stage);
+                    pc.here = n0 + 8 * (lane & 3) < a.N;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    pc.bias[i] = __shfl_sync(0xFFFFFFFFu, ch.bias, 8 * i + (lane >> 2));
-                    pc.gate[i] = __shfl_sync(0xFFFFFFFFu, ch.gate, 8 * i + (lane >> 2));
+                    for (int k = 0; k < 4; ++k) {
+                        pc.bias[k] = __shfl_sync(0xFFFFFFFFu, bias, 8 * k + (lane >> 2));
+                        pc.gate[k] = __shfl_sync(0xFFFFFFFFu, gate, 8 * k + (lane >> 2));
+                    }
+                    epilogue_pieces_share<kAct, kGrouped>(a, ta, pc, m, count, alpha);
+                } else {
+                    epilogue_rows_share<kAct, kGrouped>(a, ta, n0, lane, reinterpret_cast<float*>(stage), m,
+                                                        count, alpha, bias, gate, vec);
                 }
-                if (a.act == NVFP4KV_ACT_GELU_TANH)
-                    epilogue_pieces_share<NVFP4KV_ACT_GELU_TANH, kGrouped>(a, ta, pc, m, count, ch.alpha);
-                else if (a.act == NVFP4KV_ACT_SILU)
-                    epilogue_pieces_share<NVFP4KV_ACT_SILU, kGrouped>(a, ta, pc, m, count, ch.alpha);
-                else
-                    epilogue_pieces_share<NVFP4KV_ACT_NONE, kGrouped>(a, ta, pc, m, count, ch.alpha);
-            } else if (a.act == NVFP4KV_ACT_GELU_TANH)
-                epilogue_share<NVFP4KV_ACT_GELU_TANH, kGrouped>(a, ta, m, count, ch);
-            else if (a.act == NVFP4KV_ACT_SILU)
-                epilogue_share<NVFP4KV_ACT_SILU, kGrouped>(a, ta, m, count, ch);
-            else
-                epilogue_share<NVFP4KV_ACT_NONE, kGrouped>(a, ta, m, count, ch);
+            };
+            if (a.act == NVFP4KV_ACT_GELU_TANH) finish(IntC<NVFP4KV_ACT_GELU_TANH>());
+            else if (a.act == NVFP4KV_ACT_SILU) finish(IntC<NVFP4KV_ACT_SILU>());
+            else finish(IntC<NVFP4KV_ACT_NONE>());
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_leader<G>(smem_u32(&sh.acc_free[buf]));

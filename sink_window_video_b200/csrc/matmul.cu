@@ -255,29 +255,35 @@ __device__ __forceinline__ uint4 load16_if(const uint8_t* p, bool yes) {
     return v;
 }
 
-// z * sigmoid(v) for two values, v = z (SiLU) or 2 sqrt(2/pi) (z + 0.044715 z^3)
-// (GELU, tanh form: (1 + tanh(v/2)) / 2 = sigmoid(v)).  The two quotients share
-// one reciprocal, 1/a = b / (a b), since the special-function unit is what a
-// tile's activation waits for (1.5 instead of 2 operations a value); -v log2 e
-// is held to 60, so that a b stays finite: sigmoid below 2^-60 is lost to z's
-// last place many times over.
+// z * sigmoid(v) for four values, v = z (SiLU) or 2 sqrt(2/pi) (z + 0.044715 z^3)
+// (GELU, tanh form: (1 + tanh(v/2)) / 2 = sigmoid(v)).  The four quotients share
+// one reciprocal, 1/a = (b / (a b)) and so on, since the special-function unit is
+// what a tile's activation waits for (1.25 instead of 2 operations a value).
+// -v log2 e is held to 30, so that the product of four stays finite: a sigmoid
+// below 2^-30 becomes 2^-30, off by less than z 2^-30.
 template <int kAct>
-__device__ __forceinline__ float2 act_pair(float2 z) {
-    if (kAct == NVFP4KV_ACT_NONE) return z;
-    float2 x;
-    if (kAct == NVFP4KV_ACT_SILU) {
-        x = __fmul2_rn(z, make_float2(-1.4426950408889634f, -1.4426950408889634f));
-    } else {
-        constexpr float c1 = -1.4426950408889634f * 1.5957691216057308f;
-        constexpr float c3 = c1 * 0.044715f;
-        const float2 z2 = __fmul2_rn(z, z);
-        x = __fmul2_rn(z, __ffma2_rn(z2, make_float2(c3, c3), make_float2(c1, c1)));
-    }
-    const float2 e = make_float2(ex2f(fminf(x.x, 60.0f)), ex2f(fminf(x.y, 60.0f)));
-    const float2 d = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+__device__ __forceinline__ float2 act_exponent(float2 z) {
+    if (kAct == NVFP4KV_ACT_SILU)
+        return __fmul2_rn(z, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    constexpr float c1 = -1.4426950408889634f * 1.5957691216057308f;
+    constexpr float c3 = c1 * 0.044715f;
+    return __fmul2_rn(z, __ffma2_rn(__fmul2_rn(z, z), make_float2(c3, c3), make_float2(c1, c1)));
+}
+template <int kAct>
+__device__ __forceinline__ void act_four(float2& z0, float2& z1) {
+    if (kAct == NVFP4KV_ACT_NONE) return;
+    const float2 x0 = act_exponent<kAct>(z0), x1 = act_exponent<kAct>(z1);
+    const float2 one = make_float2(1.0f, 1.0f);
+    const float2 d0 =
+        __fadd2_rn(make_float2(ex2f(fminf(x0.x, 30.0f)), ex2f(fminf(x0.y, 30.0f))), one);
+    const float2 d1 =
+        __fadd2_rn(make_float2(ex2f(fminf(x1.x, 30.0f)), ex2f(fminf(x1.y, 30.0f))), one);
+    const float p0 = d0.x * d0.y, p1 = d1.x * d1.y;
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d.x * d.y));
-    return __fmul2_rn(z, __fmul2_rn(make_float2(d.y, d.x), make_float2(r, r)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(p0 * p1));
+    const float r0 = r * p1, r1 = r * p0;       // 1 / p0, 1 / p1
+    z0 = __fmul2_rn(z0, __fmul2_rn(make_float2(d0.y, d0.x), make_float2(r0, r0)));
+    z1 = __fmul2_rn(z1, __fmul2_rn(make_float2(d1.y, d1.x), make_float2(r1, r1)));
 }
 
 // Walks down the rows of one channel.  Four addresses take turns, each stepping
@@ -327,17 +333,25 @@ __device__ __forceinline__ void finish_tokens(const MatmulArgs& a, const uint32_
                                               const Channel& ch, Walk<float>& y, int count,
                                               const float* g) {
 #pragma unroll
-    for (int j = 0; j < C; j += 2) {
-        float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+    for (int j0 = 0; j0 < C; j0 += 4) {
+        float2 z[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            z[k] = __ffma2_rn(make_float2(__uint_as_float(v[j0 + 2 * k]),
+                                          __uint_as_float(v[j0 + 2 * k + 1])),
                               make_float2(ch.alpha, ch.alpha), make_float2(ch.bias, ch.bias));
-        z = act_pair<kAct>(z);
-        const float2 gg = kGates ? make_float2(g[j], g[j + 1]) : make_float2(g[0], g[0]);
-        if (kRes) z = __ffma2_rn(z, gg, make_float2(res[j], res[j + 1]));
-        else z = __fmul2_rn(z, gg);
-        float* y0 = y.row(j, a.ldy);
-        float* y1 = y.row(j + 1, a.ldy);
-        if (j < count) *y0 = z.x;
-        if (j + 1 < count) *y1 = z.y;
+        act_four<kAct>(z[0], z[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int j = j0 + 2 * k;
+            const float2 gg = kGates ? make_float2(g[j], g[j + 1]) : make_float2(g[0], g[0]);
+            if (kRes) z[k] = __ffma2_rn(z[k], gg, make_float2(res[j], res[j + 1]));
+            else z[k] = __fmul2_rn(z[k], gg);
+            float* y0 = y.row(j, a.ldy);
+            float* y1 = y.row(j + 1, a.ldy);
+            if (j < count) *y0 = z[k].x;
+            if (j + 1 < count) *y1 = z[k].y;
+        }
     }
 }
 
@@ -518,22 +532,26 @@ __device__ __forceinline__ void epilogue_pieces(const MatmulArgs& a, uint32_t ta
 #pragma unroll
         for (int j = 0; j < 2; ++j) {        // tokens 8 j ..
             uint32_t p[4];
+            float2 z[4];                     // channels 8 i ..
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {    // channels 8 i ..
+            for (int i = 0; i < 4; ++i) {
                 const uint32_t* s = v + 8 * (i >> 1) + 4 * j + 2 * (i & 1);
-                float2 z = __ffma2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])),
-                                      make_float2(alpha, alpha),
-                                      make_float2(pc.bias[i], pc.bias[i]));
-                z = act_pair<kAct>(z);
+                z[i] = __ffma2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])),
+                                  make_float2(alpha, alpha), make_float2(pc.bias[i], pc.bias[i]));
+            }
+            act_four<kAct>(z[0], z[1]);
+            act_four<kAct>(z[2], z[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
                 const float2 g = make_float2(pc.gate[i], pc.gate[i]);
                 if (kRes) {
                     const uint32_t w = res[4 * j + i];
-                    z = __ffma2_rn(z, g, make_float2(__uint_as_float(w << 16),
-                                                     __uint_as_float(w & 0xFFFF0000u)));
+                    z[i] = __ffma2_rn(z[i], g, make_float2(__uint_as_float(w << 16),
+                                                           __uint_as_float(w & 0xFFFF0000u)));
                 } else {
-                    z = __fmul2_rn(z, g);
+                    z[i] = __fmul2_rn(z[i], g);
                 }
-                const __nv_bfloat162 h = __floats2bfloat162_rn(z.x, z.y);
+                const __nv_bfloat162 h = __floats2bfloat162_rn(z[i].x, z[i].y);
                 p[i] = *reinterpret_cast<const uint32_t*>(&h);
             }
             stmatrix4_trans(frag + j * kHalf, p);
@@ -611,12 +629,20 @@ __device__ __forceinline__ void epilogue_rows(const MatmulArgs& a, uint32_t tadd
         tmem_wait_ld();
         __syncwarp();                        // the last tokens' rows are read
 #pragma unroll
-        for (int j = 0; j < C; j += 2) {
-            float2 z = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+        for (int j = 0; j < C; j += 4) {
+            float2 z[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                z[k] = __ffma2_rn(make_float2(__uint_as_float(v[j + 2 * k]),
+                                              __uint_as_float(v[j + 2 * k + 1])),
                                   make_float2(alpha, alpha), make_float2(bias, bias));
-            z = __fmul2_rn(act_pair<kAct>(z), make_float2(gate, gate));
-            stage[j * 32 + lane] = z.x;
-            stage[(j + 1) * 32 + lane] = z.y;
+            act_four<kAct>(z[0], z[1]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                z[k] = __fmul2_rn(z[k], make_float2(gate, gate));
+                stage[(j + 2 * k) * 32 + lane] = z[k].x;
+                stage[(j + 2 * k + 1) * 32 + lane] = z[k].y;
+            }
         }
         __syncwarp();
         uint2 now[2];
@@ -936,9 +962,25 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         const bool vec = align % 8 == 0 && a.N % 4 == 0;
         const bool pieces = align % 16 == 0 && a.N % 8 == 0 &&
                             (kGrouped || !a.gate || a.rows_per_gate >= kChunk);
+        // a tile's place and its channel's constants, loaded a tile ahead
+        struct {
+            TileAt at;
+            float scale, bias, gate;
+        } next = {};
+        const float x_scale = __ldg(a.x_scale);
+        auto look = [&](int t) {
+            next.at = tiles.at(t);
+            const int n = next.at.n0 + (warp & 3) * 32 + lane;
+            const size_t en = (size_t)next.at.e * a.N + n;
+            next.scale = __ldg(a.w_scale + next.at.e);
+            next.bias = (a.bias && n < a.N) ? __ldg(a.bias + en) : 0.0f;
+            next.gate = (a.gate && kGrouped && n < a.N) ? __ldg(a.gate + en) : 1.0f;
+        };
+        if (first_tile < total) look(first_tile);
         int i = 0;
         for (int t = first_tile; t < total; t += stride, ++i) {
-            const TileAt at = tiles.at(t);
+            const TileAt at = next.at;
+            const float alpha = x_scale * next.scale, bias = next.bias, gate = next.gate;
             const int buf = i & 1;
             constexpr int kParts = kEpiWarps / 4;
             const int part = ((at.tokens + kParts - 1) / kParts + kChunk - 1) / kChunk * kChunk;
@@ -947,10 +989,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             const int count = min(part, at.m_end - m);
             const int n0 = at.n0 + (warp & 3) * 32;
             const bool stored = n0 + lane < a.N;
-            const size_t en = (size_t)at.e * a.N + n0 + lane;
-            const float alpha = __ldg(a.x_scale) * __ldg(a.w_scale + at.e);
-            const float bias = (a.bias && stored) ? __ldg(a.bias + en) : 0.0f;
-            const float gate = (a.gate && kGrouped && stored) ? __ldg(a.gate + en) : 1.0f;
+            if (t + stride < total) look(t + stride);
             const bool got = wait_or_abort_m(smem_u32(&sh.acc_full[buf]), (uint32_t)((i >> 1) & 1),
                                              abort, a.ctl, 61u, i);
             if (!__all_sync(0xFFFFFFFFu, got)) break;

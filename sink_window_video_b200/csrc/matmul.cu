@@ -136,18 +136,25 @@ __device__ __forceinline__ void cluster_sync() {
                      : "memory");
 }
 
+// mbar_try_wait that the hardware may suspend for up to 20 us: a warp that waits
+// then takes no issue slots from the epilogue.
+__device__ __forceinline__ bool try_wait_long(uint32_t mbar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred P1;\nmbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2, %3;\n"
+        "selp.u32 %0, 1, 0, P1;\n}"
+        : "=r"(ok)
+        : "r"(mbar), "r"(parity), "r"(20000)
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ bool wait_or_abort_m(uint32_t mbar, uint32_t parity, volatile int* abort,
                                                 Control* ctl, unsigned site, unsigned step) {
-    // the clock is read only once a wait is long: reading it takes longer than
-    // most waits last
-#pragma unroll 1
-    for (int i = 0; i < 4096; ++i)
-        if (mbar_try_wait(mbar, parity)) return true;
+    if (try_wait_long(mbar, parity)) return true;
     const unsigned long long t0 = globaltimer_ns();
     while (true) {
-#pragma unroll 1
-        for (int i = 0; i < 16; ++i)
-            if (mbar_try_wait(mbar, parity)) return true;
+        if (try_wait_long(mbar, parity)) return true;
         if (*abort) return false;
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
             *abort = 1;

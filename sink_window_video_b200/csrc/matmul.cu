@@ -48,7 +48,6 @@ constexpr int kPrefetchWarp = 6;            // (7: idle)
 // warpgroups and 152 for the epilogue's two: 256 * 104 + 256 * 152 = 65536.
 constexpr int kFewRegs = 104, kManyRegs = 152;
 constexpr int kColsMM = 512;                // tensor-memory columns
-constexpr int kBox = 32;                    // token rows of one TMA load
 constexpr int kATile = kTileN * 128;        // bytes of codes of a weight tile's stage
 // Scales travel in turns of 4 steps; a K = 64 block of a 128-row group takes 512
 // bytes, 16 more apart so that a warp's 16-byte lines fall in different banks.
@@ -100,6 +99,7 @@ struct Shape {
     static_assert(kStage % 1024 == 0, "stages keep the swizzle alignment");
     static constexpr uint32_t kColSFA = 2 * TN, kColSFB = 2 * TN + 16;   // 16 and up to 32 columns
     static_assert(2 * TN + 16 + 8 * 4 <= kColsMM, "two accumulators beside the scales");
+    static constexpr int kBox = TN / G % 32 == 0 ? 32 : 56;   // token rows of one TMA load
     static_assert(TN / G % kBox == 0, "whole loads of token rows");
 };
 
@@ -1049,7 +1049,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 const TileAt at = tiles.at(t);
                 // this CTA's share of the token rows, a box at a time
                 const int m0 = at.m0 + rank * (at.tokens / G);
-                const int boxes = (at.tokens / G + kBox - 1) / kBox;
+                const int boxes = (at.tokens / G + S::kBox - 1) / S::kBox;
                 for (int s = 0; s < steps; ++s, ++it, ring.next()) {
                     // (the first pass over the ring finds the phase before the first done)
                     ok = wait_or_abort_m(smem_u32(&sh.empty[ring.at]), ring.phase ^ 1u, abort, a.ctl,
@@ -1058,14 +1058,14 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                     const uint32_t dst = stage0 + (uint32_t)ring.at * S::kStage;
                     // the leader's barrier counts both CTAs' bytes
                     uint32_t bar = smem_u32(&sh.tma_full[ring.at]);
-                    if (rank == 0) mbar_expect_tx(bar, (uint32_t)(G * (kATile + boxes * kBox * 128)));
+                    if (rank == 0) mbar_expect_tx(bar, (uint32_t)(G * (kATile + boxes * S::kBox * 128)));
                     if (G == 2) bar = leader_addr(bar);
                     tma_load_3d<G>(dst, &map_w, s * 128, at.n0, at.e, bar);
 #pragma unroll
-                    for (int i = 0; i < TN / G / kBox; ++i)
+                    for (int i = 0; i < TN / G / S::kBox; ++i)
                         if (i < boxes)
-                            tma_load_3d<G>(dst + kATile + i * kBox * 128, &map_x, s * 128,
-                                           m0 + i * kBox, 0, bar);
+                            tma_load_3d<G>(dst + kATile + i * S::kBox * 128, &map_x, s * 128,
+                                           m0 + i * S::kBox, 0, bar);
                 }
             }
             // the last uses of the stages are signalled here before the CTA leaves
@@ -1247,7 +1247,7 @@ nvfp4kv_status launch_tn(const MatmulArgs& a, const void* w_codes, const void* x
                          int sms, cudaStream_t stream) {
     CUtensorMap map_w, map_x;
     if (!make_map(&map_w, w_codes, a.K, a.N, kGrouped ? a.E : 1, kTileN) ||
-        !make_map(&map_x, x_codes, a.K, a.M, 1, kBox) || !configure<TN, G, kGrouped, kF32>(dev))
+        !make_map(&map_x, x_codes, a.K, a.M, 1, Shape<TN, G>::kBox) || !configure<TN, G, kGrouped, kF32>(dev))
         return NVFP4KV_ERR_CUDA;
     const long long n_tiles = (a.N + kTileN * G - 1) / (kTileN * G);
     // grouped: at most one more token tile per expert than the rows fill
@@ -1282,15 +1282,15 @@ int choose_tile(int M, int N, int K, int E, int sms) {
     const double steps = (K + kStageK - 1) / kStageK;
     int best = 0;
     double least = 0.0;
-    for (const int tn : {32, 64, 128, 192}) {
-        const int g = tn == 192 ? 2 : 1;
+    for (const int tn : {32, 64, 128, 192, 224}) {
+        const int g = tn > 128 ? 2 : 1;
         const double per = (double)M / E;
         // groups of all sizes: half a tile each goes to the ragged end
         const double count = E == 1 ? std::ceil(per / tn) : std::max(1.0, per / tn + 0.5);
         const double size = std::ceil(per / count / 16.0) * 16.0;
         const double tiles = count * E * ((N + kTileN * g - 1) / (kTileN * g));
         double waves = tiles / (sms / g);
-        if (E == 1 || waves < 1.0) waves = std::ceil(waves);
+        if (E <= 4 || waves < 1.0) waves = std::ceil(waves);   // many groups even out
         const double sums = steps * (g == 1 ? 250.0 + 1.1 * size : 170.0 + 1.6 * size);
         const double epilogue = 800.0 + 25.0 * size;
         const double cost = (g == 1 ? 0.0 : 1200.0) + sums + epilogue +
@@ -1314,7 +1314,8 @@ nvfp4kv_status launch_any(const MatmulArgs& a, const void* w_codes, const void* 
         case 32: return launch_tn<32, 1, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
         case 64: return launch_tn<64, 1, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
         case 128: return launch_tn<128, 1, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
-        default: return launch_tn<192, 2, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
+        case 192: return launch_tn<192, 2, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
+        default: return launch_tn<224, 2, kGrouped, kF32>(a, w_codes, x_codes, dev, sms, stream);
     }
 }
 

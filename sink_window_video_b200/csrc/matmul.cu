@@ -3,19 +3,23 @@
 // expert:
 //   Y[m][n] = R[m][n] + g * act(s_X s_W sum_k x[m][k] w[n][k] + b[n]),
 // x and w the E2M1 codes times their E4M3 block scales (16 elements along k).
+// The block products are exact in the tensor core and summed there in fp32 (5e-8
+// off 64 bits relative to the result's norm at K = 8192); the epilogue is fp32.
 //
-// The tensor core's A operand is the WEIGHT tile (128 output channels) and B
-// the token tile (TN rows of X): a tensor-memory lane is then an output
-// channel and a column a token, so one kernel serves one token and thousands
-// (the token count only sets the instruction's N), a thread's bias is one
-// register, and the 32 lanes of a warp store 32 neighbouring channels of one
-// row of Y.
+// The tensor core's A operand is the WEIGHT tile (128 output channels a CTA) and
+// B the token tile (up to TN rows of X): a tensor-memory lane is then an output
+// channel and a column a token, so that one kernel serves one token and
+// thousands: the tile's tokens, rounded up to 16, are the instruction's N.
 //
-// One persistent CTA per SM over a static tile list; roles by warp:
+// One persistent CTA per SM, or a pair of CTAs on two SMs for wide tiles
+// (cta_group::2: 256 channels x TN tokens, each CTA staging its own channels and
+// half of the tokens), over a static tile list; roles by warp:
 //   warps 0-3  block scales: global -> registers (a turn ahead) -> shared
 //              memory in the tensor core's scale layout (below)
-//   warp 4     TMA loads of both code tiles (lane 0)
-//   warp 5     tcgen05.cp of the scales into tensor memory and the MMAs (lane 0)
+//   warp 4     TMA loads of both code tiles (one elected lane)
+//   warp 5     tcgen05.cp of the scales into tensor memory and the MMAs (one
+//              elected lane; of a pair, the leader's)
+//   warp 6     the residual of the next tile into L2
 //   warps 8-15 epilogue: tensor memory -> registers -> Y
 // A stage holds 256 elements along k: 128 bytes of codes a row (one 128-byte
 // swizzle row).  The block scales (16 bytes a row and stage) travel apart, 4
@@ -25,6 +29,16 @@
 // Scale layout of one K = 64 step and 128 rows: 512 bytes, row r's four block
 // scales (bytes) at (r % 32) * 16 + (r / 32) * 4, which tcgen05.cp
 // (32x128b.warpx4) places in 4 columns of every lane quarter.
+//
+// What bounds it.  [7040, 2048] x [8192, 2048] with GELU to bf16 takes 68 us (3.5
+// PFLOP/s, the bf16 tensor peak is 1.63); without its epilogue 46 us, of which the
+// scale copies (12 tcgen05.cp a stage) are 7; without the MMAs, loads and barriers
+// alone, 33 us.  A pair halves the shared-memory writes and reads of the token
+// tile, which bound the single CTA: 192 tokens take 0.48 us a stage as a pair,
+// 0.52 as one CTA.  Kept busy for 0.3 s the same call takes 82 us: the clock falls
+// to the power limit, and what then counts is energy, the output's above all (50
+// us without the epilogue).  Small calls are latency: one row takes 5.0 us, 3.7
+// from the first CTA's start to the last one's end.
 #include <cuda.h>
 
 #include <algorithm>
@@ -57,11 +71,10 @@ constexpr int kSfGroup = 4 * kTurn * kSfBlock;
 constexpr int kChunk = 16;                  // tokens an epilogue warp takes at a time
 constexpr int kEpiBytes = 1024;             // its staging: 16 bf16 or 8 fp32 rows of 32
 constexpr int kMaxStages = 12;
-constexpr unsigned long long kLandNs = 10ull * 1000 * 1000;   // 10 ms
+// After a wait that gave up, a CTA stays this long (10 ms) for its loads to land.
+constexpr unsigned long long kLandNs = 10ull * 1000 * 1000;
 constexpr size_t kStageRoom = 216 * 1024;    // of 227 KB; the rest: offsets, barriers, alignment
 
-// TN tokens a tile; G CTAs (one, or a pair) share its MMAs: each has its own
-// 128 output channels, and stages TN / G of the token rows.
 // Instruction descriptor of the block-scaled MMA (kind::mxf4nvf4, E2M1
 // operands, E4M3 scales, fp32 D) for m x n.
 __host__ __device__ constexpr uint32_t umma_idesc_scaled(uint32_t m, uint32_t n) {
@@ -86,6 +99,8 @@ struct Ring {
     }
 };
 
+// TN tokens a tile; G CTAs (one, or a pair) share its MMAs: each has its own
+// 128 output channels, and stages TN / G of the token rows.
 template <int TN, int G>
 struct Shape {
     static constexpr int kBTile = TN / G * 128;
@@ -113,7 +128,6 @@ struct MMShared {
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
-    int bad_offsets;
 };
 
 // The address of rank 0's copy of a shared-memory object, in the cluster window.
@@ -149,6 +163,8 @@ __device__ __forceinline__ bool try_wait_long(uint32_t mbar, uint32_t parity) {
     return ok != 0;
 }
 
+// Wait for the mbarrier phase `parity`, for at most kWaitLimitNs or until another
+// role of the CTA gave up.
 __device__ __forceinline__ bool wait_or_abort_m(uint32_t mbar, uint32_t parity, volatile int* abort,
                                                 Control* ctl, unsigned site, unsigned step) {
     if (try_wait_long(mbar, parity)) return true;
@@ -267,7 +283,8 @@ __device__ __forceinline__ uint4 load16_if(const uint8_t* p, bool yes) {
 // one reciprocal, 1/a = (b / (a b)) and so on, since the special-function unit is
 // what a tile's activation waits for (1.25 instead of 2 operations a value).
 // -v log2 e is held to 30, so that the product of four stays finite: a sigmoid
-// below 2^-30 becomes 2^-30, off by less than z 2^-30.
+// below 2^-30 becomes 2^-30, off by less than z 2^-30.  (fminf also keeps a NaN
+// out of the shared reciprocal: it stays with its own value.)
 template <int kAct>
 __device__ __forceinline__ float2 act_exponent(float2 z) {
     if (kAct == NVFP4KV_ACT_SILU)

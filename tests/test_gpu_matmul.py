@@ -412,3 +412,48 @@ def test_a_block_of_the_framework(lib):
         part = dict(sh, codes=sh["codes"][a:b], scales=sh["scales"][a:b])
         checked(up[a:b], part, hosts[e], None, "gelu", None, None, C, f"group {e}")
     assert lib.workspace_status(ws) == lib.OK and cache.check_status() == lib.OK
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("bf16", [True, False], ids=["bf16", "f32"])
+def test_a_nan_stays_with_its_value_through_the_activation(lib, act, bf16):
+    """Values share a reciprocal in the activation: a NaN or infinite bias of one
+    channel and a NaN scale of one row reach that channel and row only."""
+    import torch
+    c = Case(lib, 102, 40, 96, 64, bf16=bf16, act=act)
+    c.dev["bias"][5], c.dev["bias"][50] = float("nan"), float("inf")
+    c.X.scales[7, 1] = 0x7F                      # E4M3 NaN
+    c.run()
+    torch.cuda.synchronize()
+    bad = torch.zeros(40, 96, dtype=torch.bool)
+    bad[:, 5] = bad[:, 50] = True
+    bad[7] = True
+    assert torch.equal(~torch.isfinite(c.Y.float()).cpu(), bad)
+
+
+def test_first_call_inside_a_capture(lib):
+    """A process whose first product is a captured one."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch, sink_window_video_b200 as swv
+X, W = swv.MatrixBuffer(300, 64, 1), swv.MatrixBuffer(4096, 64, 2)
+X.scales.fill_(0x38); X.tensor_scale.fill_(1); X.codes.fill_(0x22)
+W.scales.fill_(0x38); W.tensor_scale.fill_(1); W.codes.fill_(0x22)
+Y = torch.zeros(300, 4096, device="cuda")
+ws = swv.new_matrix_workspace()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    swv.matmul(X, W, Y, ws)
+g.replay()
+torch.cuda.synchronize()
+assert bool((Y == 64).all()), Y
+assert swv.workspace_status(ws) == 0
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=240)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]

@@ -278,6 +278,28 @@ __device__ __forceinline__ uint4 load16_if(const uint8_t* p, bool yes) {
     return v;
 }
 
+// The same for a residual, which may be Y itself (an ordinary load), and for a
+// constant of a channel.
+__device__ __forceinline__ uint4 load16_plain_if(const void* p, bool yes) {
+    uint4 v;
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %5, 0;\n"
+        "mov.u32 %0, 0;\nmov.u32 %1, 0;\nmov.u32 %2, 0;\nmov.u32 %3, 0;\n"
+        "@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((int)yes)
+        : "memory");
+    return v;
+}
+__device__ __forceinline__ float load_if(const float* p, bool yes, float otherwise) {
+    float v;
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\nmov.f32 %0, %3;\n@p ld.global.nc.f32 %0, [%1];\n}"
+        : "=&f"(v)
+        : "l"(p), "r"((int)yes), "f"(otherwise));
+    return v;
+}
+
 // z * sigmoid(v) for four values, v = z (SiLU) or 2 sqrt(2/pi) (z + 0.044715 z^3)
 // (GELU, tanh form: (1 + tanh(v/2)) / 2 = sigmoid(v)).  The four quotients share
 // one reciprocal, 1/a = (b / (a b)) and so on, since the special-function unit is
@@ -531,9 +553,8 @@ __device__ __forceinline__ void epilogue_pieces(const MatmulArgs& a, uint32_t ta
     constexpr uint32_t kHalf = 8 * 64;       // tokens 8 .. 15 (the swizzle repeats)
     uint4 next[2];
     auto load = [&](int left) {
-        next[0] = next[1] = make_uint4(0u, 0u, 0u, 0u);
-        if (pc.here && tok < left) next[0] = *reinterpret_cast<const uint4*>(r);
-        if (pc.here && tok + 8 < left) next[1] = *reinterpret_cast<const uint4*>(r + 8 * a.ldr);
+        next[0] = load16_plain_if(r, pc.here && tok < left);
+        next[1] = load16_plain_if(r + 8 * a.ldr, pc.here && tok + 8 < left);
         r += kChunk * a.ldr;
     };
     if (kRes) load(count);
@@ -601,7 +622,7 @@ __device__ __forceinline__ void epilogue_pieces_share(const MatmulArgs& a, uint3
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int c = pc.n0 + 8 * i + (pc.lane >> 2);
-                pc.gate[i] = c < a.N ? __ldg(a.gate + (size_t)row * a.N + c) : 0.0f;
+                pc.gate[i] = load_if(a.gate + (size_t)row * a.N + c, c < a.N, 0.0f);
             }
         }
         if (a.residual) epilogue_pieces<kAct, true>(a, taddr, pc, m, n, alpha);
@@ -997,8 +1018,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             const int n = next.at.n0 + (warp & 3) * 32 + lane;
             const size_t en = (size_t)next.at.e * a.N + n;
             next.scale = __ldg(a.w_scale + next.at.e);
-            next.bias = (a.bias && n < a.N) ? __ldg(a.bias + en) : 0.0f;
-            next.gate = (a.gate && kGrouped && n < a.N) ? __ldg(a.gate + en) : 1.0f;
+            next.bias = load_if(a.bias + en, a.bias && n < a.N, 0.0f);
+            next.gate = load_if(a.gate + en, a.gate && kGrouped && n < a.N, 1.0f);
         };
         if (first_tile < total) look(first_tile);
         int i = 0;

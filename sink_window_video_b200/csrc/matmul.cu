@@ -256,12 +256,8 @@ __device__ __forceinline__ void commit_all(uint32_t mbar) {
             : "memory");
 }
 
-// Four block scales of a row of which `left` are left (zeros past them), at a
-// 2-byte aligned address; left is even (K a multiple of 32).
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int left) {
-    const uint32_t lo = left > 0 ? __ldg(reinterpret_cast<const uint16_t*>(p)) : 0u;
-    const uint32_t hi = left > 2 ? __ldg(reinterpret_cast<const uint16_t*>(p + 2)) : 0u;
-    return lo | (hi << 16);
+__device__ __forceinline__ void put_words(uint32_t* w, const uint4& v) {
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
 }
 
 // 16 bytes at p, or zeros.  One predicated load: as a branch around a load, the
@@ -275,6 +271,22 @@ __device__ __forceinline__ uint4 load16_if(const uint8_t* p, bool yes) {
         "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
         : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
         : "l"(p), "r"((int)yes));
+    return v;
+}
+
+// `left` bytes (0 .. 16, even) from the even address p on, in the aligned words
+// from p & ~3 on: word j of them, whole or its first half, zeros where none of it
+// is left.  Nothing behind the bytes is read (before them at most the end of the
+// row before).
+__device__ __forceinline__ uint32_t load_word(const uint8_t* p, int j, int left) {
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 2);
+    const int rest = left > 0 ? left + off - 4 * j : 0;
+    uint32_t v;
+    asm volatile(
+        "{\n.reg .pred a, b;\nsetp.ge.s32 a, %2, 4;\nsetp.eq.s32 b, %2, 2;\nmov.u32 %0, 0;\n"
+        "@a ld.global.nc.u32 %0, [%1];\n@b ld.global.nc.u16 %0, [%1];\n}"
+        : "=&r"(v)
+        : "l"(p - off + 4 * j), "r"(rest));
     return v;
 }
 
@@ -927,7 +939,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         const bool withhold = blockIdx.x == 0 && warp == 0 && (a.ctl->test_flags & 1u) != 0u;
         const int g = lane & 3, q = (lane >> 2) & 3;
         const int r = 2 * warp + (lane >> 4);
-        uint4 w[kUnits];
+        uint32_t w[kUnits][5];        // a unit's words; the fifth where rows begin in mid-word
+        uint32_t odds = 0;            // units whose rows do
         const bool wide = kbytes % 16 == 0 && a.x_shift == 0;
         auto fetch = [&](const TileAt& at, int turn) {
             const int kb = turn * 64 + q * 16;
@@ -942,24 +955,27 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 const uint8_t* p = wp + (size_t)(nw >> a.w_shift) * kbytes;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    w[u] = load16_if(p, nw + 8 * u < n_end);
+                    put_words(w[u], load16_if(p, nw + 8 * u < n_end));
                     p += a.w_shift ? (u & 1) * kbytes : 8 * kbytes;
                 }
                 p = xp + (size_t)mx * kbytes;
 #pragma unroll
                 for (int u = 4; u < kUnits; ++u) {
-                    w[u] = load16_if(p, mx + 8 * (u & 3) + 128 * (u / 4 - 1) < m_end);
+                    put_words(w[u], load16_if(p, mx + 8 * (u & 3) + 128 * (u / 4 - 1) < m_end));
                     p += (u & 3) == 3 ? 104 * kbytes : 8 * kbytes;
                 }
             } else {
+                // K no multiple of 256 (or X in tiles): rows at even addresses
+                odds = 0;
 #pragma unroll
                 for (int u = 0; u < kUnits; ++u) {
                     const int i = (u < 4 ? nw : mx + 128 * (u / 4 - 1)) + 8 * (u & 3);
                     const uint8_t* p = (u < 4 ? wp : xp) +
                                        (size_t)(i >> (u < 4 ? a.w_shift : a.x_shift)) * kbytes;
-                    const int left = i < (u < 4 ? a.N : at.m_end) ? kbytes - kb : 0;
-                    w[u] = make_uint4(scale_word(p, left), scale_word(p + 4, left - 4),
-                                      scale_word(p + 8, left - 8), scale_word(p + 12, left - 12));
+                    const int left = i < (u < 4 ? a.N : at.m_end) ? max(0, min(16, kbytes - kb)) : 0;
+                    odds |= ((uint32_t)reinterpret_cast<uintptr_t>(p) >> 1 & 1u) << u;
+#pragma unroll
+                    for (int j = 0; j < 5; ++j) w[u][j] = load_word(p, j, left);
                 }
             }
         };
@@ -968,10 +984,11 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
                 uint8_t* d = line + (u / 4) * kSfGroup + (u & 3) * 128;
-                *reinterpret_cast<uint32_t*>(d) = w[u].x;
-                *reinterpret_cast<uint32_t*>(d + kSfBlock) = w[u].y;
-                *reinterpret_cast<uint32_t*>(d + 2 * kSfBlock) = w[u].z;
-                *reinterpret_cast<uint32_t*>(d + 3 * kSfBlock) = w[u].w;
+                const uint32_t shift = wide ? 0u : (odds >> u & 1u) * 16u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<uint32_t*>(d + j * kSfBlock) =
+                        wide ? w[u][j] : __funnelshift_r(w[u][j], w[u][j + 1], shift);
             }
         };
         int it = 0;
@@ -1145,7 +1162,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 if (lane == 0) arrive_leader<G>(smem_u32(&sh.acc_free[(i - 1) & 1]));
             }
         }
-        if (i > 0 && lane == 0) arrive_leader<G>(smem_u32(&sh.acc_free[(i - 1) & 1]));
+        // (no arrival for the last tile: no tile waits for its accumulator, and
+        // before its sums are full the arrival would count for the tile two before)
     } else if (warp == kMmaWarp && rank == 0) {
         // ------------------------------------------------------------ MMA issue
         // One elected lane walks the steps.  (elect.sync, not lane == 0: knowing

@@ -271,6 +271,21 @@ def test_repeated_calls_are_bit_identical(lib):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("bf16", [True, False], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,K", [(4100, 544), (4096, 512)])
+def test_every_run_with_a_residual(lib, bf16, N, K):
+    """Three to four tiles a CTA with a residual, many times over: the warp that
+    prefetches it takes part in freeing the accumulators."""
+    import torch
+    c = Case(lib, 103, 1900, N, K, w_tiles=False, residual=True, rpg=150, bf16=bf16, pad=4).run().check()
+    first = c.Y.clone()
+    for _ in range(30):
+        c.guard.t.copy_(c.before)
+        c.run()
+        torch.cuda.synchronize()
+        assert torch.equal(c.Y, first)
+
+
 def test_streams_and_graphs(lib):
     """A call on another stream than the operands', two captured graphs that
     share a workspace, replayed on new contents of the same buffers."""

@@ -58,9 +58,11 @@ constexpr int kStageK = 256;                // elements along k of one stage
 constexpr int kThreadsMM = 512;
 constexpr int kScaleWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kEpiWarp0 = 8, kEpiWarps = 8;
 constexpr int kPrefetchWarp = 6;            // (7: idle)
-// Registers of a thread: 128 at launch (65536 / 512); 104 for the first two
-// warpgroups and 152 for the epilogue's two: 256 * 104 + 256 * 152 = 65536.
-constexpr int kFewRegs = 104, kManyRegs = 152;
+// Registers of a thread: 128 at launch (65536 / 512), then so many for the first two
+// warpgroups and 256 less these for the epilogue's two: 256 * 256 = 65536.  The
+// scale warps hold a turn's 60 words; the dense fp32 epilogue wants more than the
+// others.
+constexpr int few_regs(bool grouped, bool f32) { return f32 && !grouped ? 104 : 112; }
 constexpr int kColsMM = 512;                // tensor-memory columns
 constexpr int kATile = kTileN * 128;        // bytes of codes of a weight tile's stage
 // Scales travel in turns of 4 steps; a K = 64 block of a 128-row group takes 512
@@ -925,9 +927,9 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     uint8_t* epi_base = sf_base + 2 * S::kSfStage;
 
     if (warp < kEpiWarp0)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(few_regs(kGrouped, kF32)));
     else
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(256 - few_regs(kGrouped, kF32)));
     if (warp < kTmaWarp) {
         // ------------------------------------------------------------ block scales
         // Per turn, 4 steps (64 scale bytes a row) of every 128-row group.  Unit u
@@ -981,14 +983,21 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         };
         auto put = [&](uint8_t* sf) {
             uint8_t* line = sf + 4 * q * kSfBlock + r * 16 + g * 4;
+            auto at = [&](int u, int j) {
+                return reinterpret_cast<uint32_t*>(line + (u / 4) * kSfGroup + (u & 3) * 128 +
+                                                   j * kSfBlock);
+            };
+            if (wide) {
 #pragma unroll
-            for (int u = 0; u < kUnits; ++u) {
-                uint8_t* d = line + (u / 4) * kSfGroup + (u & 3) * 128;
-                const uint32_t shift = wide ? 0u : (odds >> u & 1u) * 16u;
+                for (int u = 0; u < kUnits; ++u)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<uint32_t*>(d + j * kSfBlock) =
-                        wide ? w[u][j] : __funnelshift_r(w[u][j], w[u][j + 1], shift);
+                    for (int j = 0; j < 4; ++j) *at(u, j) = w[u][j];
+            } else {
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *at(u, j) = __funnelshift_r(w[u][j], w[u][j + 1], (odds >> u & 1u) * 16u);
             }
         };
         int it = 0;

@@ -58,11 +58,10 @@ constexpr int kStageK = 256;                // elements along k of one stage
 constexpr int kThreadsMM = 512;
 constexpr int kScaleWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kEpiWarp0 = 8, kEpiWarps = 8;
 constexpr int kPrefetchWarp = 6;            // (7: idle)
-// Registers of a thread: 128 at launch (65536 / 512), then so many for the first two
-// warpgroups and 256 less these for the epilogue's two: 256 * 256 = 65536.  The
-// scale warps hold a turn's 60 words; the dense fp32 epilogue wants more than the
-// others.
-constexpr int few_regs(bool grouped, bool f32) { return f32 && !grouped ? 104 : 112; }
+// Registers of a thread: 128 at launch (65536 / 512); 112 for the first two
+// warpgroups (the scale warps hold a turn's 60 words) and 144 for the epilogue's
+// two: 256 * 112 + 256 * 144 = 65536.
+constexpr int kFewRegs = 112, kManyRegs = 144;
 constexpr int kColsMM = 512;                // tensor-memory columns
 constexpr int kATile = kTileN * 128;        // bytes of codes of a weight tile's stage
 // Scales travel in turns of 4 steps; a K = 64 block of a 128-row group takes 512
@@ -305,6 +304,15 @@ __device__ __forceinline__ uint4 load16_plain_if(const void* p, bool yes) {
         : "memory");
     return v;
 }
+__device__ __forceinline__ float load_plain_if(const float* p, bool yes) {
+    float v;
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\nmov.f32 %0, 0f00000000;\n@p ld.global.f32 %0, [%1];\n}"
+        : "=&f"(v)
+        : "l"(p), "r"((int)yes)
+        : "memory");
+    return v;
+}
 __device__ __forceinline__ float load_if(const float* p, bool yes, float otherwise) {
     float v;
     asm volatile(
@@ -387,11 +395,10 @@ __device__ __forceinline__ void load_residual(const MatmulArgs& a, Walk<const fl
 }
 
 // The next C tokens of one channel, `count` of which exist, from their sums v and
-// residual res; the gates are g[0 .. C) where kGates, else g[0].
-template <int C, int kAct, bool kRes, bool kGates>
+// residual res, under ch.gate.
+template <int C, int kAct, bool kRes>
 __device__ __forceinline__ void finish_tokens(const MatmulArgs& a, const uint32_t* v, const float* res,
-                                              const Channel& ch, Walk<float>& y, int count,
-                                              const float* g) {
+                                              const Channel& ch, Walk<float>& y, int count) {
 #pragma unroll
     for (int j0 = 0; j0 < C; j0 += 4) {
         float2 z[2];
@@ -404,7 +411,7 @@ __device__ __forceinline__ void finish_tokens(const MatmulArgs& a, const uint32_
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int j = j0 + 2 * k;
-            const float2 gg = kGates ? make_float2(g[j], g[j + 1]) : make_float2(g[0], g[0]);
+            const float2 gg = make_float2(ch.gate, ch.gate);
             if (kRes) z[k] = __ffma2_rn(z[k], gg, make_float2(res[j], res[j + 1]));
             else z[k] = __fmul2_rn(z[k], gg);
             float* y0 = y.row(j, a.ldy);
@@ -439,36 +446,41 @@ __device__ __forceinline__ void epilogue_run(const MatmulArgs& a, uint32_t taddr
             load_residual<kChunk>(a, r, next, count - kChunk + here);
         }
         tmem_wait_ld();
-        finish_tokens<kChunk, kAct, kRes, false>(a, v, res, ch, y, count + here, &ch.gate);
+        finish_tokens<kChunk, kAct, kRes>(a, v, res, ch, y, count + here);
     }
 }
 
 // `count` tokens from row m on, their gates looked up one by one.
 template <int kAct>
-__device__ __forceinline__ void epilogue_gates(const MatmulArgs& a, uint32_t taddr, Channel& ch, int m,
-                                               int count) {
+__device__ __forceinline__ void epilogue_gates(const MatmulArgs& a, uint32_t taddr, const Channel& ch,
+                                               int m, int count) {
     constexpr int C = 4;
-    Walk<float> y(ch.y, a.ldy);
-    Walk<const float> r(ch.r, a.ldr);
-    int q = m / a.rows_per_gate, rem = m - q * a.rows_per_gate;
+    float* y = ch.y;
+    const float* r = ch.r;
 #pragma unroll 1
-    for (; count > 0; count -= C, taddr += C) {
-        const int here = ch.stored ? count : 0;
+    for (; count > 0; count -= C, taddr += C, m += C) {
         uint32_t v[C];
         tmem_ld4(taddr, v);
-        float res[C] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (a.residual) load_residual<C>(a, r, res, here);
-        float g[C];
+        float res[C], g[C];
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-            if (j < here) g[j] = __ldg(a.gate + (size_t)q * a.N + ch.n);
-            if (++rem == a.rows_per_gate) {
-                rem = 0;
-                ++q;
-            }
+            const bool here = ch.stored && j < count;
+            res[j] = load_plain_if(r + j * a.ldr, here && a.residual);
+            g[j] = load_if(a.gate + (size_t)((m + j) / a.rows_per_gate) * a.N + ch.n, here, 0.0f);
         }
         tmem_wait_ld();
-        finish_tokens<C, kAct, true, true>(a, v, res, ch, y, here, g);
+        float2 z[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            z[k] = __ffma2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])),
+                              make_float2(ch.alpha, ch.alpha), make_float2(ch.bias, ch.bias));
+        act_four<kAct>(z[0], z[1]);
+        const float f[C] = {z[0].x, z[0].y, z[1].x, z[1].y};
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+            if (ch.stored && j < count) y[j * a.ldy] = fmaf(f[j], g[j], res[j]);
+        y += C * a.ldy;
+        r += C * a.ldr;
         __syncwarp();
     }
 }
@@ -927,9 +939,9 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     uint8_t* epi_base = sf_base + 2 * S::kSfStage;
 
     if (warp < kEpiWarp0)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(few_regs(kGrouped, kF32)));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     else
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(256 - few_regs(kGrouped, kF32)));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
     if (warp < kTmaWarp) {
         // ------------------------------------------------------------ block scales
         // Per turn, 4 steps (64 scale bytes a row) of every 128-row group.  Unit u

@@ -356,56 +356,64 @@ ACT_NONE, ACT_GELU_TANH, ACT_SILU = 0, 1, 2      # nvfp4kv_activation
 
 def _row_stride(t, name, M, N):
     """Row stride of a [M, N] tensor whose rows are contiguous."""
-    if t.shape != (M, N) or (N > 1 and t.stride(1) != 1) or (M > 1 and t.stride(0) < N):
+    ld, inner = t.stride() if t.dim() == 2 else (0, 0)
+    if t.shape != (M, N) or (N > 1 and inner != 1) or (M > 1 and ld < N):
         raise ValueError(f"{name} must be a [{M}, {N}] tensor with contiguous rows, "
                          f"got {tuple(t.shape)} strides {t.stride()}")
-    return t.stride(0) if M > 1 else N
+    return ld if M > 1 else N
+
+
+def _vector_ptr(t, shape, device, name):
+    """Address of an optional contiguous float32 operand on the output's device."""
+    if t is None:
+        return None
+    _check_part(t, shape, _torch().float32, name)
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}")
+    return t.data_ptr()
 
 
 def _matmul_args(X, W, Y, ws, bias, activation, gate, gate_rows, rows_per_gate, residual, lead):
     """Checks that the products share; the epilogue, Y's row stride and dtype."""
-    M, N, y_dtype = X.M, W.M, _dtype_code(Y)
+    M, N, y_dtype, device = X.M, W.M, _dtype_code(Y), Y.get_device()
     if X.N != W.N:
         raise ValueError(f"X has {X.N} columns and W {W.N}")
-    ep = Epilogue(None, activation, None, rows_per_gate, None, 0)
-    operands = [X._codes, W._codes, ws]
-    if bias is not None:
-        _check_part(bias, lead + (N,), _torch().float32, "bias")
-        ep.bias = bias.data_ptr()
-        operands.append(bias)
-    if gate is not None:
-        _check_part(gate, (gate_rows, N), _torch().float32, "gate")
-        ep.gate = gate.data_ptr()
-        operands.append(gate)
+    if not device == X._codes.get_device() == W._codes.get_device() == ws.get_device():
+        raise ValueError(f"operands on {X.codes.device}, {W.codes.device} and {ws.device}, "
+                         f"Y on {Y.device}")
+    r_ptr, ldr = None, 0
     if residual is not None:
         if residual.dtype != Y.dtype:
             raise TypeError(f"residual is {residual.dtype}, Y {Y.dtype}")
-        ep.ld_residual = _row_stride(residual, "residual", M, N)
-        ep.residual = residual.data_ptr()
-        operands.append(residual)
-    device = Y.get_device()
-    for t in operands:
-        if t.get_device() != device:
-            raise ValueError(f"operands on {t.device} and {Y.device}")
+        if residual.get_device() != device:
+            raise ValueError(f"residual is on {residual.device}")
+        r_ptr, ldr = residual.data_ptr(), _row_stride(residual, "residual", M, N)
+    ep = Epilogue(_vector_ptr(bias, lead + (N,), device, "bias"), activation,
+                  _vector_ptr(gate, (gate_rows, N), device, "gate"), rows_per_gate, r_ptr, ldr)
     return ep, _row_stride(Y, "Y", M, N), y_dtype
 
 
-def _on_device_of(Y, stream, call):
-    """call(stream handle) with Y's device current; stream None is that
-    device's current stream."""
-    torch, device = _torch(), Y.get_device()
+def _stream_on(device, stream):
+    """Stream handle for a call whose output is on `device` (an index); None is
+    that device's current stream."""
     if device < 0:
-        raise ValueError(f"Y is on {Y.device}")
+        raise ValueError("the output is not on a CUDA device")
     if stream is None:
         # current_stream(device).cuda_stream without the Stream object, whose
         # making takes half as long as the launch
-        stream = torch._C._cuda_getCurrentRawStream(device)
+        return _torch()._C._cuda_getCurrentRawStream(device)
+    return _stream(stream)
+
+
+def _call_on(device, where, fn, *args):
+    """fn(*args) with `device` current."""
+    cuda = _torch().cuda
+    if cuda.current_device() == device:
+        status = fn(*args)
     else:
-        stream = _stream(stream)
-    if torch.cuda.current_device() == device:
-        return call(stream)
-    with torch.cuda.device(device):
-        return call(stream)
+        with cuda.device(device):
+            status = fn(*args)
+    _check(status, where)
 
 
 def matmul(X: "MatrixBuffer", W: "MatrixBuffer", Y, ws, bias=None, activation=ACT_NONE, gate=None,
@@ -421,9 +429,10 @@ def matmul(X: "MatrixBuffer", W: "MatrixBuffer", Y, ws, bias=None, activation=AC
     gate_rows = -(-X.M // rows_per_gate) if gate is not None else 0
     ep, ldy, y_dtype = _matmul_args(X, W, Y, ws, bias, activation, gate, gate_rows, rows_per_gate,
                                     residual, ())
-    _check(_on_device_of(Y, stream, lambda s: load().nvfp4kv_matmul(
-        X.view, W.view, X.M, W.M, X.N, ep, Y.data_ptr(), ldy, y_dtype, ws.data_ptr(), s)),
-        "nvfp4kv_matmul")
+    device = Y.get_device()
+    stream = _stream_on(device, stream)
+    _call_on(device, "nvfp4kv_matmul", load().nvfp4kv_matmul, X.view, W.view, X.M, W.M, X.N, ep,
+             Y.data_ptr(), ldy, y_dtype, ws.data_ptr(), stream)
 
 
 def grouped_matmul(X: "MatrixBuffer", W: "GroupedMatrixBuffer", offsets, Y, ws, bias=None,
@@ -434,13 +443,15 @@ def grouped_matmul(X: "MatrixBuffer", W: "GroupedMatrixBuffer", offsets, Y, ws, 
     if not isinstance(W, GroupedMatrixBuffer):
         raise TypeError(f"W is a {type(W).__name__}, not a GroupedMatrixBuffer")
     _check_part(offsets, (W.E + 1,), _torch().int32, "offsets")
-    if offsets.device != Y.device:
-        raise ValueError(f"operands on {offsets.device} and {Y.device}")
+    device = Y.get_device()
+    if offsets.get_device() != device:
+        raise ValueError(f"offsets are on {offsets.device}")
     ep, ldy, y_dtype = _matmul_args(X, W, Y, ws, bias, activation, gate, W.E, 0, residual,
                                     (W.E,))
-    _check(_on_device_of(Y, stream, lambda s: load().nvfp4kv_grouped_matmul(
-        X.view, W.view, W.E, X.M, W.M, X.N, offsets.data_ptr(), ep, Y.data_ptr(), ldy,
-        y_dtype, ws.data_ptr(), s)), "nvfp4kv_grouped_matmul")
+    stream = _stream_on(device, stream)
+    _call_on(device, "nvfp4kv_grouped_matmul", load().nvfp4kv_grouped_matmul, X.view, W.view, W.E,
+             X.M, W.M, X.N, offsets.data_ptr(), ep, Y.data_ptr(), ldy, y_dtype, ws.data_ptr(),
+             stream)
 
 
 def attention_launches(n_chunks, T_c, H, T_q, d=HEAD_DIM) -> int:

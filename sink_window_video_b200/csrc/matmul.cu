@@ -30,7 +30,7 @@
 // scales (bytes) at (r % 32) * 16 + (r / 32) * 4, which tcgen05.cp
 // (32x128b.warpx4) places in 4 columns of every lane quarter.
 //
-// What bounds it.  [7040, 2048] x [8192, 2048] with GELU to bf16 takes 68 us (3.5
+// What bounds it.  [7040, 2048] x [8192, 2048] with GELU to bf16 takes 67 us (3.5
 // PFLOP/s, the bf16 tensor peak is 1.63); without its epilogue 46 us, of which the
 // scale copies (12 tcgen05.cp a stage) are 7; without the MMAs, loads and barriers
 // alone, 33 us.  A pair halves the shared-memory writes and reads of the token

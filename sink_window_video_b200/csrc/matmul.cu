@@ -275,6 +275,15 @@ __device__ __forceinline__ uint4 load16_if(const uint8_t* p, bool yes) {
     return v;
 }
 
+__device__ __forceinline__ uint32_t load4_if(const uint8_t* p, bool yes) {
+    uint32_t v;
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\nmov.u32 %0, 0;\n@p ld.global.nc.u32 %0, [%1];\n}"
+        : "=&r"(v)
+        : "l"(p), "r"((int)yes));
+    return v;
+}
+
 // `left` bytes (0 .. 16, even) from the even address p on, in the aligned words
 // from p & ~3 on: word j of them, whole or its first half, zeros where none of it
 // is left.  Nothing behind the bytes is read (before them at most the end of the
@@ -979,17 +988,31 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                     p += (u & 3) == 3 ? 104 * kbytes : 8 * kbytes;
                 }
             } else {
-                // K no multiple of 256 (or X in tiles): rows at even addresses
+                // K no multiple of 256 (or X in tiles): rows at even addresses; by
+                // whole words where K is a multiple of 64
                 odds = 0;
-#pragma unroll
-                for (int u = 0; u < kUnits; ++u) {
+                auto unit = [&](int u, int& left) {
                     const int i = (u < 4 ? nw : mx + 128 * (u / 4 - 1)) + 8 * (u & 3);
-                    const uint8_t* p = (u < 4 ? wp : xp) +
-                                       (size_t)(i >> (u < 4 ? a.w_shift : a.x_shift)) * kbytes;
-                    const int left = i < (u < 4 ? a.N : at.m_end) ? max(0, min(16, kbytes - kb)) : 0;
-                    odds |= ((uint32_t)reinterpret_cast<uintptr_t>(p) >> 1 & 1u) << u;
+                    left = i < (u < 4 ? a.N : at.m_end) ? max(0, min(16, kbytes - kb)) : 0;
+                    return (u < 4 ? wp : xp) +
+                           (size_t)(i >> (u < 4 ? a.w_shift : a.x_shift)) * kbytes;
+                };
+                int left;
+                if (kbytes % 4 == 0) {
 #pragma unroll
-                    for (int j = 0; j < 5; ++j) w[u][j] = load_word(p, j, left);
+                    for (int u = 0; u < kUnits; ++u) {
+                        const uint8_t* p = unit(u, left);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[u][j] = load4_if(p + 4 * j, left > 4 * j);
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) {
+                        const uint8_t* p = unit(u, left);
+                        odds |= ((uint32_t)reinterpret_cast<uintptr_t>(p) >> 1 & 1u) << u;
+#pragma unroll
+                        for (int j = 0; j < 5; ++j) w[u][j] = load_word(p, j, left);
+                    }
                 }
             }
         };

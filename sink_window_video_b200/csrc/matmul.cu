@@ -284,19 +284,12 @@ __device__ __forceinline__ uint32_t load4_if(const uint8_t* p, bool yes) {
     return v;
 }
 
-// `left` bytes (0 .. 16, even) from the even address p on, in the aligned words
-// from p & ~3 on: word j of them, whole or its first half, zeros where none of it
-// is left.  Nothing behind the bytes is read (before them at most the end of the
-// row before).
-__device__ __forceinline__ uint32_t load_word(const uint8_t* p, int j, int left) {
-    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 2);
-    const int rest = left > 0 ? left + off - 4 * j : 0;
+__device__ __forceinline__ uint32_t load2_if(const uint8_t* p, bool yes) {
     uint32_t v;
     asm volatile(
-        "{\n.reg .pred a, b;\nsetp.ge.s32 a, %2, 4;\nsetp.eq.s32 b, %2, 2;\nmov.u32 %0, 0;\n"
-        "@a ld.global.nc.u32 %0, [%1];\n@b ld.global.nc.u16 %0, [%1];\n}"
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\nmov.u32 %0, 0;\n@p ld.global.nc.u16 %0, [%1];\n}"
         : "=&r"(v)
-        : "l"(p - off + 4 * j), "r"(rest));
+        : "l"(p), "r"((int)yes));
     return v;
 }
 
@@ -962,8 +955,9 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         const bool withhold = blockIdx.x == 0 && warp == 0 && (a.ctl->test_flags & 1u) != 0u;
         const int g = lane & 3, q = (lane >> 2) & 3;
         const int r = 2 * warp + (lane >> 4);
-        uint32_t w[kUnits][5];        // a unit's words; the fifth where rows begin in mid-word
-        uint32_t odds = 0;            // units whose rows do
+        uint32_t w[kUnits][5];        // a unit's words, and the half word it ends in
+        uint32_t odds = 0;            // units whose rows begin in mid-word
+        int turn_left = 0;            // bytes of this lane's 16 that a row has
         const bool wide = kbytes % 16 == 0 && a.x_shift == 0;
         auto fetch = [&](const TileAt& at, int turn) {
             const int kb = turn * 64 + q * 16;
@@ -991,9 +985,10 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 // K no multiple of 256 (or X in tiles): rows at even addresses; by
                 // whole words where K is a multiple of 64
                 odds = 0;
+                turn_left = max(0, min(16, kbytes - kb));
                 auto unit = [&](int u, int& left) {
                     const int i = (u < 4 ? nw : mx + 128 * (u / 4 - 1)) + 8 * (u & 3);
-                    left = i < (u < 4 ? a.N : at.m_end) ? max(0, min(16, kbytes - kb)) : 0;
+                    left = i < (u < 4 ? a.N : at.m_end) ? turn_left : 0;
                     return (u < 4 ? wp : xp) +
                            (size_t)(i >> (u < 4 ? a.w_shift : a.x_shift)) * kbytes;
                 };
@@ -1009,9 +1004,16 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
 #pragma unroll
                     for (int u = 0; u < kUnits; ++u) {
                         const uint8_t* p = unit(u, left);
-                        odds |= ((uint32_t)reinterpret_cast<uintptr_t>(p) >> 1 & 1u) << u;
+                        // the aligned words that the row fills, and the half word
+                        // that it may end in (at most one); nothing behind the row
+                        // is read
+                        const int odd = (int)(reinterpret_cast<uintptr_t>(p) >> 1 & 1);
+                        odds |= (uint32_t)odd << u;
+                        p -= 2 * odd;
+                        const int bytes = left > 0 ? left + 2 * odd : 0;
 #pragma unroll
-                        for (int j = 0; j < 5; ++j) w[u][j] = load_word(p, j, left);
+                        for (int j = 0; j < 4; ++j) w[u][j] = load4_if(p + 4 * j, bytes >= 4 * j + 4);
+                        w[u][4] = load2_if(p + (bytes & ~3), (bytes & 2) != 0);
                     }
                 }
             }
@@ -1022,17 +1024,22 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 return reinterpret_cast<uint32_t*>(line + (u / 4) * kSfGroup + (u & 3) * 128 +
                                                    j * kSfBlock);
             };
-            if (wide) {
+            if (kbytes % 4 == 0) {
 #pragma unroll
                 for (int u = 0; u < kUnits; ++u)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) *at(u, j) = w[u][j];
             } else {
 #pragma unroll
-                for (int u = 0; u < kUnits; ++u)
+                for (int u = 0; u < kUnits; ++u) {
+                    const int odd = (int)(odds >> u & 1u), bytes = turn_left + 2 * odd;
+                    const int half = (bytes & 2) ? bytes >> 2 : 5;     // the half word's place
+                    uint32_t v[5];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *at(u, j) = __funnelshift_r(w[u][j], w[u][j + 1], (odds >> u & 1u) * 16u);
+                    for (int j = 0; j < 5; ++j) v[j] = half == j ? w[u][4] : j < 4 ? w[u][j] : 0u;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) *at(u, j) = __funnelshift_r(v[j], v[j + 1], 16 * odd);
+                }
             }
         };
         int it = 0;

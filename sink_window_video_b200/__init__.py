@@ -162,13 +162,16 @@ def _ptr(x):
     return x.data_ptr()
 
 
+@functools.cache
+def _dtype_codes():
+    return {_torch().float32: F32, _torch().bfloat16: BF16}
+
+
 def _dtype_code(t):
-    import torch
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"output dtype {t.dtype} is not float32 or bfloat16")
+    code = _dtype_codes().get(t.dtype)
+    if code is None:
+        raise TypeError(f"output dtype {t.dtype} is not float32 or bfloat16")
+    return code
 
 
 def _check_qo(Q, O, H, d):
@@ -273,44 +276,77 @@ def _check_part(t, shape, dtype, name):
                          f"got {t.dtype} {tuple(t.shape)}")
 
 
+_PARTS = ("codes", "scales", "tensor_scale")
+
+
 class _Parts:
-    """The three device buffers of quantized matrices and their view.  A buffer
-    that is assigned anew is put into the view too."""
+    """The three device buffers of quantized matrices and their view.  A tensor
+    that is assigned to one of them is checked as `parts` are.  Storage, shape and
+    type of a tensor can change in place too (Tensor.set_, .data), and so can
+    the sizes: each call asks the tensors where they are, and has them checked and
+    the view made anew where an address or a size is not the view's."""
 
-    def _set_parts(self, parts, shapes, mode, device):
-        torch = _torch()
-        names = ("codes", "scales", "tensor_scale")
-        dtypes = (torch.uint8, torch.uint8, torch.float32)
+    E = 1                        # matrices in the buffers
+    _kept = None, None           # what the last view was made of, and the view
+
+    def _set_parts(self, parts, device):
         if parts is None:
-            parts = [torch.zeros(s, dtype=t, device=device) for s, t in zip(shapes, dtypes)]
-        else:
-            for t, s, d, name in zip(parts, shapes, dtypes, names):
-                _check_part(t, s, d, name)
-                if t.device != parts[0].device:
-                    raise ValueError(f"parts on {parts[0].device} and {t.device}")
-        self.view = MatrixView(None, None, None, mode)
-        for name, t in zip(names, parts):
+            parts = [_torch().zeros(s, dtype=t, device=device)
+                     for s, t in zip(self._shapes(), self._dtypes())]
+        for name, t in zip(_PARTS, parts):
             setattr(self, name, t)
+            if t.device != parts[0].device:
+                raise ValueError(f"parts on {parts[0].device} and {t.device}")
 
-    def _part(name):
-        def put(self, t):
-            setattr(self, "_" + name, t)
-            setattr(self.view, name, t.data_ptr())
-        return property(lambda self: getattr(self, "_" + name), put)
+    def _dtypes(self):
+        u8 = _torch().uint8
+        return u8, u8, _torch().float32
 
-    codes, scales, tensor_scale = _part("codes"), _part("scales"), _part("tensor_scale")
-    del _part
+    def _check_part(self, i, t):
+        _check_part(t, self._shapes()[i], self._dtypes()[i], _PARTS[i])
+
+    def __setattr__(self, name, value):
+        if name in _PARTS:
+            self._check_part(_PARTS.index(name), value)
+        object.__setattr__(self, name, value)
+
+    def __getstate__(self):
+        # copies and pickles hold the tensors; a view of theirs is made at a call
+        return {k: v for k, v in self.__dict__.items() if k != "_kept"}
+
+    @property
+    def view(self):
+        """The buffers and the mode as they are now.  A view that was handed out
+        is never changed."""
+        c, s, t = self.codes, self.scales, self.tensor_scale
+        # a contiguous tensor at the same address with as many bytes is the same
+        # memory, on the same device
+        now = (c.data_ptr(), s.data_ptr(), t.data_ptr(), c.nbytes, s.nbytes, t.nbytes,
+               self.E, self.M, self.N, self.mode)
+        made_of, view = self._kept
+        if now != made_of or not (c.is_contiguous() and s.is_contiguous() and t.is_contiguous()):
+            for i, part in enumerate((c, s, t)):
+                self._check_part(i, part)
+            if not c.device == s.device == t.device:
+                raise ValueError(f"parts on {c.device}, {s.device} and {t.device}")
+            view = MatrixView(*now[:3], self.mode)
+            self._kept = now, view
+        return view
 
 
 class MatrixBuffer(_Parts):
     """Device buffers of a quantized [M, N] matrix: codes [M, N/2] (uint8),
     scales ([M, N/16] for 1D blocks, [M/16, N/16] for 2D tiles), tensor scale.
-    `parts`: a (codes, scales, tensor_scale) that holds one already."""
+    `parts`: a (codes, scales, tensor_scale) that holds one already.  Copies
+    (copy.copy) share the tensors, not later assignments."""
 
     def __init__(self, M, N, mode, device="cuda", parts=None):
         self.M, self.N, self.mode = M, N, mode
-        brows = M if mode == BLOCKS_1D else M // 16
-        self._set_parts(parts, ((M, N // 2), (brows, N // 16), (1,)), mode, device)
+        self._set_parts(parts, device)
+
+    def _shapes(self):
+        M, N = self.M, self.N
+        return (M, N // 2), (M if self.mode == BLOCKS_1D else M // 16, N // 16), (1,)
 
     def to_host(self):
         return dict(codes=self.codes.cpu().numpy(), scales=self.scales.cpu().numpy(),
@@ -329,9 +365,9 @@ def quantize_matrix(X, out: "MatrixBuffer", ws, stream=None):
     """NVFP4 quantization of a bf16 [M, N] matrix with Four-Over-Six (1D row
     blocks or 2D 16 x 16 tiles, out.mode)."""
     M, N = X.shape
-    _check(load().nvfp4kv_quantize_matrix(_ptr(X), M, N, out.mode, _ptr(out.codes),
-                                          _ptr(out.scales), _ptr(out.tensor_scale), _ptr(ws),
-                                          _stream(stream)),
+    v = out.view
+    _check(load().nvfp4kv_quantize_matrix(_ptr(X), M, N, v.mode, v.codes, v.scales,
+                                          v.tensor_scale, _ptr(ws), _stream(stream)),
            "nvfp4kv_quantize_matrix")
 
 
@@ -342,8 +378,11 @@ class GroupedMatrixBuffer(_Parts):
 
     def __init__(self, E, M, N, mode, device="cuda", parts=None):
         self.E, self.M, self.N, self.mode = E, M, N, mode
-        brows = M if mode == BLOCKS_1D else M // 16
-        self._set_parts(parts, ((E, M, N // 2), (E, brows, N // 16), (E,)), mode, device)
+        self._set_parts(parts, device)
+
+    def _shapes(self):
+        E, M, N = self.E, self.M, self.N
+        return (E, M, N // 2), (E, M if self.mode == BLOCKS_1D else M // 16, N // 16), (E,)
 
     def expert(self, e) -> MatrixBuffer:
         """Matrix e, for quantize_matrix to write."""
@@ -356,8 +395,9 @@ ACT_NONE, ACT_GELU_TANH, ACT_SILU = 0, 1, 2      # nvfp4kv_activation
 
 def _row_stride(t, name, M, N):
     """Row stride of a [M, N] tensor whose rows are contiguous."""
-    ld, inner = t.stride() if t.dim() == 2 else (0, 0)
-    if t.shape != (M, N) or (N > 1 and inner != 1) or (M > 1 and ld < N):
+    same = t.shape == (M, N)
+    ld, inner = t.stride() if same else (0, 0)
+    if not same or (N > 1 and inner != 1) or (M > 1 and ld < N):
         raise ValueError(f"{name} must be a [{M}, {N}] tensor with contiguous rows, "
                          f"got {tuple(t.shape)} strides {t.stride()}")
     return ld if M > 1 else N
@@ -373,12 +413,15 @@ def _vector_ptr(t, shape, device, name):
     return t.data_ptr()
 
 
-def _matmul_args(X, W, Y, ws, bias, activation, gate, gate_rows, rows_per_gate, residual, lead):
-    """Checks that the products share; the epilogue, Y's row stride and dtype."""
-    M, N, y_dtype, device = X.M, W.M, _dtype_code(Y), Y.get_device()
+def _matmul_args(X, W, Y, device, ws, bias, activation, gate, gate_rows, rows_per_gate, residual,
+                 lead):
+    """Checks that the products share; the views of X and W, the epilogue, Y's row
+    stride and dtype."""
+    M, N, y_dtype = X.M, W.M, _dtype_code(Y)
     if X.N != W.N:
         raise ValueError(f"X has {X.N} columns and W {W.N}")
-    if not device == X._codes.get_device() == W._codes.get_device() == ws.get_device():
+    x, w = X.view, W.view
+    if not device == X.codes.get_device() == W.codes.get_device() == ws.get_device():
         raise ValueError(f"operands on {X.codes.device}, {W.codes.device} and {ws.device}, "
                          f"Y on {Y.device}")
     r_ptr, ldr = None, 0
@@ -390,7 +433,7 @@ def _matmul_args(X, W, Y, ws, bias, activation, gate, gate_rows, rows_per_gate, 
         r_ptr, ldr = residual.data_ptr(), _row_stride(residual, "residual", M, N)
     ep = Epilogue(_vector_ptr(bias, lead + (N,), device, "bias"), activation,
                   _vector_ptr(gate, (gate_rows, N), device, "gate"), rows_per_gate, r_ptr, ldr)
-    return ep, _row_stride(Y, "Y", M, N), y_dtype
+    return x, w, ep, _row_stride(Y, "Y", M, N), y_dtype
 
 
 def _stream_on(device, stream):
@@ -427,11 +470,11 @@ def matmul(X: "MatrixBuffer", W: "MatrixBuffer", Y, ws, bias=None, activation=AC
     if gate is not None and rows_per_gate < 1:
         raise ValueError(f"rows_per_gate {rows_per_gate} with a gate")
     gate_rows = -(-X.M // rows_per_gate) if gate is not None else 0
-    ep, ldy, y_dtype = _matmul_args(X, W, Y, ws, bias, activation, gate, gate_rows, rows_per_gate,
-                                    residual, ())
     device = Y.get_device()
+    x, w, ep, ldy, y_dtype = _matmul_args(X, W, Y, device, ws, bias, activation, gate, gate_rows,
+                                          rows_per_gate, residual, ())
     stream = _stream_on(device, stream)
-    _call_on(device, "nvfp4kv_matmul", load().nvfp4kv_matmul, X.view, W.view, X.M, W.M, X.N, ep,
+    _call_on(device, "nvfp4kv_matmul", load().nvfp4kv_matmul, x, w, X.M, W.M, X.N, ep,
              Y.data_ptr(), ldy, y_dtype, ws.data_ptr(), stream)
 
 
@@ -446,10 +489,10 @@ def grouped_matmul(X: "MatrixBuffer", W: "GroupedMatrixBuffer", offsets, Y, ws, 
     device = Y.get_device()
     if offsets.get_device() != device:
         raise ValueError(f"offsets are on {offsets.device}")
-    ep, ldy, y_dtype = _matmul_args(X, W, Y, ws, bias, activation, gate, W.E, 0, residual,
-                                    (W.E,))
+    x, w, ep, ldy, y_dtype = _matmul_args(X, W, Y, device, ws, bias, activation, gate, W.E, 0,
+                                          residual, (W.E,))
     stream = _stream_on(device, stream)
-    _call_on(device, "nvfp4kv_grouped_matmul", load().nvfp4kv_grouped_matmul, X.view, W.view, W.E,
+    _call_on(device, "nvfp4kv_grouped_matmul", load().nvfp4kv_grouped_matmul, x, w, W.E,
              X.M, W.M, X.N, offsets.data_ptr(), ep, Y.data_ptr(), ldy, y_dtype, ws.data_ptr(),
              stream)
 

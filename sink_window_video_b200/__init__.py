@@ -393,6 +393,13 @@ class GroupedMatrixBuffer(_Parts):
 ACT_NONE, ACT_GELU_TANH, ACT_SILU = 0, 1, 2      # nvfp4kv_activation
 
 
+def _check_kinds(X, W, w_kind):
+    if not isinstance(X, MatrixBuffer):
+        raise TypeError(f"X is a {type(X).__name__}, not a MatrixBuffer")
+    if not isinstance(W, w_kind):
+        raise TypeError(f"W is a {type(W).__name__}, not a {w_kind.__name__}")
+
+
 def _row_stride(t, name, M, N):
     """Row stride of a [M, N] tensor whose rows are contiguous."""
     same = t.shape == (M, N)
@@ -465,8 +472,7 @@ def matmul(X: "MatrixBuffer", W: "MatrixBuffer", Y, ws, bias=None, activation=AC
     W [N, K] into Y [M, N] (float32 or bf16, contiguous rows, any row stride).
     bias [N] float32; gate [ceil(M / rows_per_gate), N] float32, row m takes
     gate row m // rows_per_gate; residual [M, N] of Y's dtype (may be Y)."""
-    if not isinstance(W, MatrixBuffer):
-        raise TypeError(f"W is a {type(W).__name__}, not a MatrixBuffer")
+    _check_kinds(X, W, MatrixBuffer)
     if gate is not None and rows_per_gate < 1:
         raise ValueError(f"rows_per_gate {rows_per_gate} with a gate")
     gate_rows = -(-X.M // rows_per_gate) if gate is not None else 0
@@ -483,8 +489,7 @@ def grouped_matmul(X: "MatrixBuffer", W: "GroupedMatrixBuffer", offsets, Y, ws, 
     """matmul by groups of rows: rows offsets[e] .. offsets[e + 1] - 1 of X
     times matrix e of W; rows outside the groups of Y are left as they are.
     offsets: int32 [E + 1] on the device; bias and gate [E, N] float32."""
-    if not isinstance(W, GroupedMatrixBuffer):
-        raise TypeError(f"W is a {type(W).__name__}, not a GroupedMatrixBuffer")
+    _check_kinds(X, W, GroupedMatrixBuffer)
     _check_part(offsets, (W.E + 1,), _torch().int32, "offsets")
     device = Y.get_device()
     if offsets.get_device() != device:

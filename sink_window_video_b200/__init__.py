@@ -329,6 +329,10 @@ class _Parts:
                 self._check_part(i, part)
             if not c.device == s.device == t.device:
                 raise ValueError(f"parts on {c.device}, {s.device} and {t.device}")
+            # (beyond 32 bits ctypes would pass on another number)
+            if self.mode not in (BLOCKS_1D, TILES_2D) or max(self.E, self.M, self.N) >= 1 << 31:
+                raise NvFp4KvError(ERR_INVALID_ARG, f"{self.E} x [{self.M}, {self.N}], block "
+                                                    f"shape {self.mode}")
             view = MatrixView(*now[:3], self.mode)
             self._kept = now, view
         return view
@@ -431,6 +435,8 @@ def _matmul_args(X, W, Y, device, ws, bias, activation, gate, gate_rows, rows_pe
     if not device == X.codes.get_device() == W.codes.get_device() == ws.get_device():
         raise ValueError(f"operands on {X.codes.device}, {W.codes.device} and {ws.device}, "
                          f"Y on {Y.device}")
+    if not ACT_NONE <= activation <= ACT_SILU:
+        raise NvFp4KvError(ERR_INVALID_ARG, f"activation {activation}")
     r_ptr, ldr = None, 0
     if residual is not None:
         if residual.dtype != Y.dtype:
@@ -475,6 +481,8 @@ def matmul(X: "MatrixBuffer", W: "MatrixBuffer", Y, ws, bias=None, activation=AC
     _check_kinds(X, W, MatrixBuffer)
     if gate is not None and rows_per_gate < 1:
         raise ValueError(f"rows_per_gate {rows_per_gate} with a gate")
+    # one gate row for all holds for any number from M on, beyond 32 bits too
+    rows_per_gate = min(rows_per_gate, X.M)
     gate_rows = -(-X.M // rows_per_gate) if gate is not None else 0
     device = Y.get_device()
     x, w, ep, ldy, y_dtype = _matmul_args(X, W, Y, device, ws, bias, activation, gate, gate_rows,

@@ -919,6 +919,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             carry += __shfl_sync(0xFFFFFFFFu, inc, 31);
         }
         bad = __any_sync(0xFFFFFFFFu, bad);
+        __syncwarp();            // the last group's lane has written s_tile[E]
         if (lane == 0) {
             s_tile[0] = 0;
             if (bad) {

@@ -1,0 +1,26 @@
+"""GPU NVFP4 matrix products at the edges of their kernel's tiles, roles and
+groups, against float64 on the same codes and scales."""
+import pytest
+
+from test_gpu_matmul import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("E", [1, 2, 31, 32, 33, 64, 1000, 1024])
+def test_bad_offsets_of_the_last_group(lib, E):
+    """The last group's offsets break the rule, whatever place it has among the
+    32 that are looked at together: reported, nothing written."""
+    import torch
+    T, good = 40, [0] * E + [40]
+    c = Case(lib, 200 + E, T, 64, 64, offsets=good)
+    for last in (T + 1, 1 << 30, -1, -(1 << 31)):
+        c.off = torch.tensor([0] * E + [last], dtype=torch.int32, device="cuda")
+        for _ in range(5):
+            c.run()
+        torch.cuda.synchronize()
+        assert lib.workspace_status(c.ws) == lib.ERR_INVALID_ARG
+        assert torch.equal(c.guard.t.view(torch.uint8), c.before.view(torch.uint8))
+        c.guard.assert_intact()
+    c.off = torch.tensor(good, dtype=torch.int32, device="cuda")
+    c.run().check("after bad offsets")

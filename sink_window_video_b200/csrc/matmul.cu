@@ -315,6 +315,13 @@ __device__ __forceinline__ float load_plain_if(const float* p, bool yes) {
         : "memory");
     return v;
 }
+// (or v stays as it is)
+__device__ __forceinline__ void load_plain_onto(float& v, const float* p, bool yes) {
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\n@p ld.global.f32 %0, [%1];\n}"
+                 : "+f"(v)
+                 : "l"(p), "r"((int)yes)
+                 : "memory");
+}
 __device__ __forceinline__ float load_if(const float* p, bool yes, float otherwise) {
     float v;
     asm volatile(
@@ -376,6 +383,10 @@ struct Walk {
     }
 };
 
+// The tensor-memory loads and their wait (and stmatrix, ldmatrix) are instructions
+// of a whole warp.  What stands before them may part its lanes (a predicate of a
+// lane's channel or token), so each loop below that loads has a __syncwarp() before.
+
 // What an epilogue thread keeps of its tile: its channel n, that channel's
 // constants, and where the next token's result and residual are.
 struct Channel {
@@ -392,7 +403,7 @@ __device__ __forceinline__ void load_residual(const MatmulArgs& a, Walk<const fl
 #pragma unroll
     for (int j = 0; j < C; ++j) {
         const float* p = r.row(j, a.ldr);
-        if (j < count) res[j] = *p;
+        load_plain_onto(res[j], p, j < count);
     }
 }
 
@@ -430,7 +441,7 @@ __device__ __forceinline__ void finish_tokens(const MatmulArgs& a, const uint32_
 template <int kAct, bool kRes>
 __device__ __forceinline__ void epilogue_run(const MatmulArgs& a, uint32_t taddr, Channel& ch,
                                              int count) {
-    float next[kRes ? kChunk : 1];
+    float next[kRes ? kChunk : 1] = {};
     Walk<float> y(ch.y, a.ldy);
     Walk<const float> r(ch.r, kRes ? a.ldr : 0);
     ch.y += (size_t)count * a.ldy;
@@ -439,14 +450,15 @@ __device__ __forceinline__ void epilogue_run(const MatmulArgs& a, uint32_t taddr
     if (kRes) load_residual<kChunk>(a, r, next, count + here);
 #pragma unroll 1
     for (; count > 0; count -= kChunk, taddr += kChunk) {
-        uint32_t v[kChunk];
-        tmem_ld16(taddr, v);
         float res[kRes ? kChunk : 1];
         if (kRes) {
 #pragma unroll
             for (int j = 0; j < kChunk; ++j) res[j] = next[j];
             load_residual<kChunk>(a, r, next, count - kChunk + here);
         }
+        uint32_t v[kChunk];
+        __syncwarp();
+        tmem_ld16(taddr, v);
         tmem_wait_ld();
         finish_tokens<kChunk, kAct, kRes>(a, v, res, ch, y, count + here);
     }
@@ -462,6 +474,7 @@ __device__ __forceinline__ void epilogue_gates(const MatmulArgs& a, uint32_t tad
 #pragma unroll 1
     for (; count > 0; count -= C, taddr += C, m += C) {
         uint32_t v[C];
+        __syncwarp();
         tmem_ld4(taddr, v);
         float res[C], g[C];
 #pragma unroll
@@ -483,7 +496,6 @@ __device__ __forceinline__ void epilogue_gates(const MatmulArgs& a, uint32_t tad
             if (ch.stored && j < count) y[j * a.ldy] = fmaf(f[j], g[j], res[j]);
         y += C * a.ldy;
         r += C * a.ldr;
-        __syncwarp();
     }
 }
 
@@ -508,7 +520,6 @@ __device__ __forceinline__ void epilogue_share(const MatmulArgs& a, uint32_t tad
         }
         if (a.residual) epilogue_run<kAct, true>(a, taddr, ch, n);
         else epilogue_run<kAct, false>(a, taddr, ch, n);
-        __syncwarp();
         taddr += n;
         m += n;
         count -= n;
@@ -589,9 +600,9 @@ __device__ __forceinline__ void epilogue_pieces(const MatmulArgs& a, uint32_t ta
 #pragma unroll 1
     for (; count > 0; count -= kChunk, taddr += kChunk) {
         uint32_t v[16], res[8];
+        __syncwarp();                        // the last chunk's pieces are read and stored
         tmem_ld_frag2(taddr, v);
         tmem_ld_frag2(taddr + (16u << 16), v + 8);
-        __syncwarp();                        // the last chunk's pieces are read
         if (kRes) {
             sts16(own, next[0]);
             sts16(own + kHalf, next[1]);
@@ -698,9 +709,9 @@ __device__ __forceinline__ void epilogue_rows(const MatmulArgs& a, uint32_t tadd
 #pragma unroll 1
     for (; count > 0; count -= C, taddr += C) {
         uint32_t v[C];
+        __syncwarp();                        // the last tokens' rows are read and stored
         tmem_ld8(taddr, v);
         tmem_wait_ld();
-        __syncwarp();                        // the last tokens' rows are read
 #pragma unroll
         for (int j = 0; j < C; j += 4) {
             float2 z[2];

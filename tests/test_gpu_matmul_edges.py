@@ -24,3 +24,14 @@ def test_bad_offsets_of_the_last_group(lib, E):
         c.guard.assert_intact()
     c.off = torch.tensor(good, dtype=torch.int32, device="cuda")
     c.run().check("after bad offsets")
+
+
+@pytest.mark.parametrize("bf16", [True, False], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rpg", [0, 3, 17, 40])
+@pytest.mark.parametrize("N", [8, 40, 100, 137])
+def test_channels_that_end_inside_a_warp(lib, bf16, rpg, N):
+    """Some lanes of a warp have a channel and others none, at the loads of the
+    gate, of the residual and of the sums: every epilogue, several chunks."""
+    for act in ("none", "gelu"):
+        Case(lib, 300 + N + rpg, 77, N, 96, w_tiles=False, bf16=bf16, act=act, rpg=rpg,
+             residual=rpg != 17, pad=N % 2).run().check(f"{act} {N} {rpg}")

@@ -576,11 +576,12 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     return v;
 }
 
-// `count` tokens from row m on under pc.gate, accumulators in tensor memory at
-// taddr.
+// Tokens skip .. count - 1 from row m on under pc.gate, accumulators in tensor
+// memory at taddr, whole chunks into the tile: the fragments' load takes columns in
+// pairs, and an odd column is a misaligned address to it.
 template <int kAct, bool kRes>
 __device__ __forceinline__ void epilogue_pieces(const MatmulArgs& a, uint32_t taddr, const Pieces& pc,
-                                                int m, int count, float alpha) {
+                                                int m, int skip, int count, float alpha) {
     const int tok = pc.lane >> 2, piece = pc.lane & 3;
     const size_t first = (size_t)(m + tok), col = (size_t)(pc.n0 + 8 * piece);
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.Y) + first * a.ldy + col;
@@ -591,14 +592,15 @@ __device__ __forceinline__ void epilogue_pieces(const MatmulArgs& a, uint32_t ta
     const uint32_t own = pc.stage + Pieces::at(tok, piece);
     constexpr uint32_t kHalf = 8 * 64;       // tokens 8 .. 15 (the swizzle repeats)
     uint4 next[2];
-    auto load = [&](int left) {
-        next[0] = load16_plain_if(r, pc.here && tok < left);
-        next[1] = load16_plain_if(r + 8 * a.ldr, pc.here && tok + 8 < left);
+    auto mine = [&](int t) { return pc.here && t >= skip && t < count; };
+    auto load = [&](int ahead) {
+        next[0] = load16_plain_if(r, mine(tok + ahead));
+        next[1] = load16_plain_if(r + 8 * a.ldr, mine(tok + ahead + 8));
         r += kChunk * a.ldr;
     };
-    if (kRes) load(count);
+    if (kRes) load(0);
 #pragma unroll 1
-    for (; count > 0; count -= kChunk, taddr += kChunk) {
+    for (; count > 0; count -= kChunk, skip -= kChunk, taddr += kChunk) {
         uint32_t v[16], res[8];
         __syncwarp();                        // the last chunk's pieces are read and stored
         tmem_ld_frag2(taddr, v);
@@ -606,7 +608,7 @@ __device__ __forceinline__ void epilogue_pieces(const MatmulArgs& a, uint32_t ta
         if (kRes) {
             sts16(own, next[0]);
             sts16(own + kHalf, next[1]);
-            load(count - kChunk);
+            load(kChunk);
             __syncwarp();
             ldmatrix4_trans(frag, res);
             ldmatrix4_trans(frag + kHalf, res + 4);
@@ -641,22 +643,24 @@ __device__ __forceinline__ void epilogue_pieces(const MatmulArgs& a, uint32_t ta
             stmatrix4_trans(frag + j * kHalf, p);
         }
         __syncwarp();
-        if (pc.here && tok < count) *reinterpret_cast<uint4*>(y) = lds16(own);
-        if (pc.here && tok + 8 < count) *reinterpret_cast<uint4*>(y + 8 * a.ldy) = lds16(own + kHalf);
+        if (mine(tok)) *reinterpret_cast<uint4*>(y) = lds16(own);
+        if (mine(tok + 8)) *reinterpret_cast<uint4*>(y + 8 * a.ldy) = lds16(own + kHalf);
         y += kChunk * a.ldy;
     }
 }
 
-// One warp's share of a bf16 tile in pieces: stretches of tokens under one gate.
+// One warp's share of a bf16 tile in pieces: stretches of tokens under one gate, a
+// chunk that two of them share once for each.
 template <int kAct, bool kGrouped>
 __device__ __forceinline__ void epilogue_pieces_share(const MatmulArgs& a, uint32_t taddr, Pieces& pc,
                                                       int m, int count, float alpha) {
     const bool by_row = !kGrouped && a.gate;
+    int skip = 0;                            // tokens of the chunk at m that are done
 #pragma unroll 1
-    while (count > 0) {
+    while (skip < count) {
         int n = count;
         if (by_row) {
-            const int row = m / a.rows_per_gate;
+            const int row = (m + skip) / a.rows_per_gate;
             n = (int)min((long long)count, (long long)(row + 1) * a.rows_per_gate - m);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -664,11 +668,13 @@ __device__ __forceinline__ void epilogue_pieces_share(const MatmulArgs& a, uint3
                 pc.gate[i] = load_if(a.gate + (size_t)row * a.N + c, c < a.N, 0.0f);
             }
         }
-        if (a.residual) epilogue_pieces<kAct, true>(a, taddr, pc, m, n, alpha);
-        else epilogue_pieces<kAct, false>(a, taddr, pc, m, n, alpha);
-        taddr += n;
-        m += n;
-        count -= n;
+        if (a.residual) epilogue_pieces<kAct, true>(a, taddr, pc, m, skip, n, alpha);
+        else epilogue_pieces<kAct, false>(a, taddr, pc, m, skip, n, alpha);
+        const int whole = n / kChunk * kChunk;
+        taddr += whole;
+        m += whole;
+        count -= whole;
+        skip = n - whole;
     }
 }
 
@@ -686,12 +692,13 @@ __device__ __forceinline__ uint2 pack4(const float* f) {
     return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// `count` tokens from row m on, accumulators in tensor memory at taddr.  gate: of
-// this lane's channel n0 + lane; kGates: looked up for each token instead.
+// Tokens skip .. count - 1 from row m on, accumulators in tensor memory at taddr (a
+// multiple of 8 tokens into the tile).  gate: of this lane's channel n0 + lane;
+// kGates: looked up for each token instead.
 template <int kAct, bool kRes, bool kGates>
 __device__ __forceinline__ void epilogue_rows(const MatmulArgs& a, uint32_t taddr, int n0, int lane,
-                                              float* stage, int m, int count, float alpha, float bias,
-                                              float gate, bool vec) {
+                                              float* stage, int m, int skip, int count, float alpha,
+                                              float bias, float gate, bool vec) {
     using T = __nv_bfloat16;
     constexpr int C = 8;
     const int tok = lane >> 3, col = 4 * (lane & 7);
@@ -699,15 +706,16 @@ __device__ __forceinline__ void epilogue_rows(const MatmulArgs& a, uint32_t tadd
     T* y = static_cast<T*>(a.Y) + (size_t)(m + tok) * a.ldy + n0 + col;
     const T* r = static_cast<const T*>(a.residual) + (size_t)(m + tok) * a.ldr + n0 + col;
     uint2 next[2];
-    auto load = [&](int left) {
+    auto is_mine = [&](int t) { return t >= skip && t < count && here > 0; };
+    auto load = [&](int ahead) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            if (tok + 4 * h < left && here > 0) next[h] = *reinterpret_cast<const uint2*>(r + 4 * h * a.ldr);
+            if (is_mine(tok + ahead + 4 * h)) next[h] = *reinterpret_cast<const uint2*>(r + 4 * h * a.ldr);
         r += C * a.ldr;
     };
-    if (kRes && vec) load(count);
+    if (kRes && vec) load(0);
 #pragma unroll 1
-    for (; count > 0; count -= C, taddr += C) {
+    for (; count > 0; count -= C, skip -= C, taddr += C) {
         uint32_t v[C];
         __syncwarp();                        // the last tokens' rows are read and stored
         tmem_ld8(taddr, v);
@@ -733,11 +741,11 @@ __device__ __forceinline__ void epilogue_rows(const MatmulArgs& a, uint32_t tadd
         if (kRes && vec) {
             now[0] = next[0];
             now[1] = next[1];
-            load(count - C);
+            load(C);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const bool mine = tok + 4 * h < count && here > 0;
+            const bool mine = is_mine(tok + 4 * h);
             const float4 q = *reinterpret_cast<const float4*>(stage + (tok + 4 * h) * 32 + col);
             float f[4] = {q.x, q.y, q.z, q.w};
             if (kGates && mine) {
@@ -778,29 +786,32 @@ __device__ __forceinline__ void epilogue_rows_share(const MatmulArgs& a, uint32_
     const bool by_row = !kGrouped && a.gate;
     if (by_row && a.rows_per_gate < kChunk) {
         if (a.residual)
-            epilogue_rows<kAct, true, true>(a, taddr, n0, lane, stage, m, count, alpha, bias, 1.0f,
-                                                  vec);
+            epilogue_rows<kAct, true, true>(a, taddr, n0, lane, stage, m, 0, count, alpha, bias, 1.0f,
+                                            vec);
         else
-            epilogue_rows<kAct, false, true>(a, taddr, n0, lane, stage, m, count, alpha, bias, 1.0f,
-                                                   vec);
+            epilogue_rows<kAct, false, true>(a, taddr, n0, lane, stage, m, 0, count, alpha, bias, 1.0f,
+                                             vec);
         return;
     }
+    constexpr int C = 8;
+    int skip = 0;                            // tokens of the 8 at m that are done
 #pragma unroll 1
-    while (count > 0) {
+    while (skip < count) {
         int n = count;
         if (by_row) {
-            const int row = m / a.rows_per_gate;
+            const int row = (m + skip) / a.rows_per_gate;
             n = (int)min((long long)count, (long long)(row + 1) * a.rows_per_gate - m);
             gate = n0 + lane < a.N ? __ldg(a.gate + (size_t)row * a.N + n0 + lane) : 0.0f;
         }
         if (a.residual)
-            epilogue_rows<kAct, true, false>(a, taddr, n0, lane, stage, m, n, alpha, bias, gate, vec);
+            epilogue_rows<kAct, true, false>(a, taddr, n0, lane, stage, m, skip, n, alpha, bias, gate, vec);
         else
-            epilogue_rows<kAct, false, false>(a, taddr, n0, lane, stage, m, n, alpha, bias, gate,
-                                                    vec);
-        taddr += n;
-        m += n;
-        count -= n;
+            epilogue_rows<kAct, false, false>(a, taddr, n0, lane, stage, m, skip, n, alpha, bias, gate, vec);
+        const int whole = n / C * C;
+        taddr += whole;
+        m += whole;
+        count -= whole;
+        skip = n - whole;
     }
 }
 

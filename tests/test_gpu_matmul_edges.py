@@ -35,3 +35,18 @@ def test_channels_that_end_inside_a_warp(lib, bf16, rpg, N):
     for act in ("none", "gelu"):
         Case(lib, 300 + N + rpg, 77, N, 96, w_tiles=False, bf16=bf16, act=act, rpg=rpg,
              residual=rpg != 17, pad=N % 2).run().check(f"{act} {N} {rpg}")
+
+
+@pytest.mark.parametrize("rpg", [17, 19, 23, 31, 33, 97])
+@pytest.mark.parametrize("N", [144, 132, 137])
+def test_gates_that_change_at_odd_rows(lib, N, rpg):
+    """A gate that ends inside a chunk of tokens, at an odd place: in bf16 as whole
+    pieces of a row, in parts of 4 and by element, with the residual in place."""
+    for residual in (False, True):
+        c = Case(lib, 500 + N + rpg, 333, N, 160, w_tiles=False, act="silu", rpg=rpg,
+                 residual=residual, pad=8 if N == 144 else 4)
+        if residual:
+            c.Y.copy_(c.R)
+            c.R = c.Y
+            c.before = c.guard.t.clone()
+        c.run().check(f"{N} {rpg} {residual}")

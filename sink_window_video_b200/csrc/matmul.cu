@@ -18,7 +18,8 @@
 //              memory in the tensor core's scale layout (below)
 //   warp 4     TMA loads of both code tiles (one elected lane)
 //   warp 5     tcgen05.cp of the scales into tensor memory and the MMAs (one
-//              elected lane; of a pair, the leader's)
+//              elected lane; of a pair, the leader's: the other's hands its CTA's
+//              scales over)
 //   warp 6     the residual of the next tile into L2
 //   warps 8-15 epilogue: tensor memory -> registers -> Y
 // A stage holds 256 elements along k: 128 bytes of codes a row (one 128-byte
@@ -122,6 +123,7 @@ struct Shape {
 struct MMShared {
     uint64_t tma_full[kMaxStages];
     uint64_t sf_full[2];
+    uint64_t sf_own[2];      // of a pair's second CTA: its scales, before the leader's sf_full
     uint64_t sf_empty[2];
     uint64_t empty[kMaxStages];
     uint64_t acc_full[2];
@@ -140,7 +142,14 @@ __device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-// Arrive on the leader's barrier (for one CTA, its own).
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+                 : "memory");
+}
+// Arrive on the leader's barrier (for one CTA, its own) to free an accumulator.  No
+// memory changes hands, so nothing has to be released to the other CTA: the sums
+// are in registers (tcgen05.wait::ld) before the arrival, and what may overwrite
+// them is issued after it was seen.
 template <int G>
 __device__ __forceinline__ void arrive_leader(uint32_t mbar) {
     if (G == 1) mbar_arrive(mbar);
@@ -152,26 +161,39 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // mbar_try_wait that the hardware may suspend for up to 20 us: a warp that waits
-// then takes no issue slots from the epilogue.
+// then takes no issue slots from the epilogue.  kCluster: acquires what another CTA
+// released (the MMA lane the second CTA's scales; what TMA and the tensor core bring
+// or free comes with their own arrivals).
+template <bool kCluster>
 __device__ __forceinline__ bool try_wait_long(uint32_t mbar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred P1;\nmbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2, %3;\n"
-        "selp.u32 %0, 1, 0, P1;\n}"
-        : "=r"(ok)
-        : "r"(mbar), "r"(parity), "r"(20000)
-        : "memory");
+    if (kCluster)
+        asm volatile(
+            "{\n.reg .pred P1;\n"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 P1, [%1], %2, %3;\n"
+            "selp.u32 %0, 1, 0, P1;\n}"
+            : "=r"(ok)
+            : "r"(mbar), "r"(parity), "r"(20000)
+            : "memory");
+    else
+        asm volatile(
+            "{\n.reg .pred P1;\nmbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2, %3;\n"
+            "selp.u32 %0, 1, 0, P1;\n}"
+            : "=r"(ok)
+            : "r"(mbar), "r"(parity), "r"(20000)
+            : "memory");
     return ok != 0;
 }
 
 // Wait for the mbarrier phase `parity`, for at most kWaitLimitNs or until another
 // role of the CTA gave up.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_or_abort_m(uint32_t mbar, uint32_t parity, volatile int* abort,
                                                 Control* ctl, unsigned site, unsigned step) {
-    if (try_wait_long(mbar, parity)) return true;
+    if (try_wait_long<kCluster>(mbar, parity)) return true;
     const unsigned long long t0 = globaltimer_ns();
     while (true) {
-        if (try_wait_long(mbar, parity)) return true;
+        if (try_wait_long<kCluster>(mbar, parity)) return true;
         if (*abort) return false;
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
             *abort = 1;
@@ -904,7 +926,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             mbar_init(smem_u32(&sh.empty[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh.sf_full[i]), kScaleWarps * G);
+            mbar_init(smem_u32(&sh.sf_full[i]), kScaleWarps + (G - 1));
+            mbar_init(smem_u32(&sh.sf_own[i]), kScaleWarps);
             mbar_init(smem_u32(&sh.sf_empty[i]), 1);
             mbar_init(smem_u32(&sh.acc_full[i]), 1);
             mbar_init(smem_u32(&sh.acc_free[i]), (kEpiWarps + (a.residual ? 1 : 0)) * G);
@@ -1079,7 +1102,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 put(sf_base + st * S::kSfStage);
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0 && !(withhold && it == 0)) arrive_leader<G>(smem_u32(&sh.sf_full[st]));
+                if (lane == 0 && !(withhold && it == 0))
+                    mbar_arrive(smem_u32(rank == 0 ? &sh.sf_full[st] : &sh.sf_own[st]));
                 if (turn + 1 < turns) fetch(at, turn + 1);
                 else if (t + stride < total) fetch(tiles.at(t + stride), 0);
             }
@@ -1257,8 +1281,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 const uint32_t d = tmem + (uint32_t)acc.at * TN;
                 const uint32_t idesc = umma_idesc_scaled(G * kTileN, (uint32_t)tiles.at(t).tokens);
                 for (int s = 0; s < steps; s += kTurn, turn.next()) {
-                    ok = wait_or_abort_m(smem_u32(&sh.sf_full[turn.at]), turn.phase, abort, a.ctl, 64u,
-                                         s);
+                    ok = wait_or_abort_m<(G > 1)>(smem_u32(&sh.sf_full[turn.at]), turn.phase, abort,
+                                                  a.ctl, 64u, s);
                     if (!ok) break;
                     const uint32_t sf = sf0 + (uint32_t)turn.at * S::kSfStage;
                     const int n = min(kTurn, steps - s);
@@ -1281,6 +1305,9 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                                 tmem_cp_scales<G>(tmem + S::kColSFB + 8u * j + 4u * (q - 1),
                                                   ds + (uint64_t)((kSfGroup * q + kSfBlock * j) >> 4));
                         }
+                        // the turn's scales are in tensor memory once its last copies are
+                        // done, a step before its last MMAs
+                        if (k == n - 1) commit_all<G>(smem_u32(&sh.sf_empty[turn.at]));
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             mma_scaled<G>(d, da + 2u * j, db + 2u * j, idesc, (s | k | j) ? 1u : 0u,
@@ -1288,12 +1315,28 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                         commit_all<G>(smem_u32(&sh.empty[ring.at]));
                     }
                     if (!ok) break;
-                    commit_all<G>(smem_u32(&sh.sf_empty[turn.at]));
                 }
                 if (ok) commit_all<G>(smem_u32(&sh.acc_full[acc.at]));
             }
             commit_own<G>(smem_u32(&sh.drain));
             mbar_wait(smem_u32(&sh.drain), 0u);
+        }
+        __syncwarp();
+    } else if (G == 2 && warp == kMmaWarp) {
+        // ------------------------------------------------------------ scales of a pair
+        // The leader's copies read the second CTA's scales in that CTA's shared
+        // memory, so they are handed over at cluster scope, once a turn.  This warp
+        // releases them, since a release waits for what its warp has in flight (the
+        // scale warps: the next turn's loads; [7040, 8192] x [2048, 8192] took 77 us
+        // with the release in those, 65 to 67 so).
+        if (elect_one()) {
+            Ring<2> turn;
+            bool ok = true;
+            for (int t = first_tile; t < total && ok; t += stride)
+                for (int k = 0; k < turns && ok; ++k, turn.next()) {
+                    ok = wait_or_abort_m(smem_u32(&sh.sf_own[turn.at]), turn.phase, abort, a.ctl, 64u, k);
+                    if (ok) mbar_arrive_release_cluster(leader_addr(smem_u32(&sh.sf_full[turn.at])));
+                }
         }
         __syncwarp();
     }

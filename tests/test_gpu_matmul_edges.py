@@ -50,3 +50,22 @@ def test_gates_that_change_at_odd_rows(lib, N, rpg):
             c.R = c.Y
             c.before = c.guard.t.clone()
         c.run().check(f"{N} {rpg} {residual}")
+
+
+@pytest.mark.parametrize("bf16", [True, False], ids=["bf16", "f32"])
+def test_pairs_of_ctas_hand_over_their_scales(lib, bf16):
+    """A pair's second CTA stores its share of the block scales for the first one's
+    MMAs, turn by turn: two products with scales of their own take turns, and
+    each result stays bit for bit what it was."""
+    import torch
+    cases = [Case(lib, 400 + i, 2300, 4100, 1312, w_tiles=False, bf16=bf16, residual=i == 1)
+             for i in range(2)]
+    first = []
+    for c in cases:
+        c.run().check("first")
+        first.append(c.Y.clone())
+    for _ in range(20):
+        for c, y in zip(cases, first):
+            c.guard.t.copy_(c.before)
+            c.run()
+            assert torch.equal(c.Y, y)

@@ -1108,6 +1108,11 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 else if (t + stride < total) fetch(tiles.at(t + stride), 0);
             }
         }
+        // the last turns are signalled as done here before the CTA leaves (the
+        // leader's commits arrive in both)
+        for (int i = max(it - 2, 0); i < it && ok; ++i)
+            ok = wait_or_abort_m(smem_u32(&sh.sf_empty[i & 1]), (uint32_t)((i >> 1) & 1), abort, a.ctl,
+                                 60u, i);
     } else if (warp >= kEpiWarp0) {
         // ------------------------------------------------------------ epilogue
         // warp = lane quarter (warp % 4) of one part of the tile's tokens

@@ -69,3 +69,19 @@ def test_pairs_of_ctas_hand_over_their_scales(lib, bf16):
             c.guard.t.copy_(c.before)
             c.run()
             assert torch.equal(c.Y, y)
+
+
+@pytest.mark.parametrize("K", [32, 1056, 2080])
+def test_launches_close_behind_one_another(lib, K):
+    """Pairs of CTAs with one turn of scales a tile, or a last turn of one step:
+    launch upon launch on the same multiprocessors, each leaving none of its
+    signals to the next."""
+    import torch
+    c = Case(lib, 600 + K, 1900, 4096, K, bf16=False).run().check(str(K))
+    first = c.Y.clone()
+    for _ in range(5):
+        c.guard.t.copy_(c.before)
+        for _ in range(40):
+            c.run()
+        assert torch.equal(c.Y, first)
+    assert lib.workspace_status(c.ws) == lib.OK

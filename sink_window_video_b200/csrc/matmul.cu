@@ -353,13 +353,18 @@ __device__ __forceinline__ float load_if(const float* p, bool yes, float otherwi
     return v;
 }
 
-// z * sigmoid(v) for four values, v = z (SiLU) or 2 sqrt(2/pi) (z + 0.044715 z^3)
-// (GELU, tanh form: (1 + tanh(v/2)) / 2 = sigmoid(v)).  The four quotients share
-// one reciprocal, 1/a = (b / (a b)) and so on, since the special-function unit is
-// what a tile's activation waits for (1.25 instead of 2 operations a value).
-// -v log2 e is held to 30, so that the product of four stays finite: a sigmoid
-// below 2^-30 becomes 2^-30, off by less than z 2^-30.  (fminf also keeps a NaN
-// out of the shared reciprocal: it stays with its own value.)
+// z * sigmoid(v), v = z (SiLU) or 2 sqrt(2/pi) (z + 0.044715 z^3) (GELU, tanh form:
+// (1 + tanh(v/2)) / 2 = sigmoid(v)).  With x = -v log2 e the sigmoid is 1 / (1 + 2^x).
+// The special-function unit is what a tile's activation waits for, so four quotients
+// share one reciprocal, 1/a = b / (a b) and so on (1.25 instead of 2 operations a
+// value).  That holds while the product of four is finite and none is NaN, which
+// would reach all four: x at most 30, that is z at least kLeast.  Where a z of the
+// warp is below or NaN, each value takes a reciprocal of its own, 0 from 2^x =
+// infinity on.  Large negative z then end in -0, and minus infinity in NaN (infinity
+// times 0), as the formulas do.  The warp votes on that for a chunk, staying together
+// for the loads and stores behind; the shared quotients are formed meanwhile (an
+// epilogue warp has one other on its scheduler to hide a vote), and where they do not
+// hold the sums are read from tensor memory once more.
 template <int kAct>
 __device__ __forceinline__ float2 act_exponent(float2 z) {
     if (kAct == NVFP4KV_ACT_SILU)
@@ -368,21 +373,78 @@ __device__ __forceinline__ float2 act_exponent(float2 z) {
     constexpr float c3 = c1 * 0.044715f;
     return __fmul2_rn(z, __ffma2_rn(__fmul2_rn(z, z), make_float2(c3, c3), make_float2(c1, c1)));
 }
+// 1 + 2^x of two values
 template <int kAct>
-__device__ __forceinline__ void act_four(float2& z0, float2& z1) {
-    if (kAct == NVFP4KV_ACT_NONE) return;
-    const float2 x0 = act_exponent<kAct>(z0), x1 = act_exponent<kAct>(z1);
-    const float2 one = make_float2(1.0f, 1.0f);
-    const float2 d0 =
-        __fadd2_rn(make_float2(ex2f(fminf(x0.x, 30.0f)), ex2f(fminf(x0.y, 30.0f))), one);
-    const float2 d1 =
-        __fadd2_rn(make_float2(ex2f(fminf(x1.x, 30.0f)), ex2f(fminf(x1.y, 30.0f))), one);
-    const float p0 = d0.x * d0.y, p1 = d1.x * d1.y;
+__device__ __forceinline__ float2 act_divisor(float2 z) {
+    const float2 x = act_exponent<kAct>(z);
+    return __fadd2_rn(make_float2(ex2f(x.x), ex2f(x.y)), make_float2(1.0f, 1.0f));
+}
+__device__ __forceinline__ float rcp_approx(float a) {
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(p0 * p1));
-    const float r0 = r * p1, r1 = r * p0;       // 1 / p0, 1 / p1
-    z0 = __fmul2_rn(z0, __fmul2_rn(make_float2(d0.y, d0.x), make_float2(r0, r0)));
-    z1 = __fmul2_rn(z1, __fmul2_rn(make_float2(d1.y, d1.x), make_float2(r1, r1)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+    return r;
+}
+// the least of three, or NaN
+__device__ __forceinline__ float least_of(float a, float b, float c) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// Whether all z of the warp, P pairs a lane, are where four may share a reciprocal:
+// x(-20.7) = 29.9 and x(-5.5) = 29.8.
+template <int kAct, int P>
+__device__ __forceinline__ bool warp_shares(const float2 (&z)[P]) {
+    constexpr float kLeast = kAct == NVFP4KV_ACT_SILU ? -20.7f : -5.5f;
+    float least = 0.0f;
+#pragma unroll
+    for (int k = 0; k < P; ++k) least = least_of(least, z[k].x, z[k].y);
+    return __all_sync(0xFFFFFFFFu, least >= kLeast);
+}
+template <int kAct, int P>
+__device__ __forceinline__ void activate_shared(float2 (&z)[P]) {
+#pragma unroll
+    for (int k = 0; k < P; k += 2) {
+        const float2 d0 = act_divisor<kAct>(z[k]), d1 = act_divisor<kAct>(z[k + 1]);
+        const float p0 = d0.x * d0.y, p1 = d1.x * d1.y;
+        const float r = rcp_approx(p0 * p1);
+        const float r0 = r * p1, r1 = r * p0;       // 1 / p0, 1 / p1
+        z[k] = __fmul2_rn(z[k], __fmul2_rn(make_float2(d0.y, d0.x), make_float2(r0, r0)));
+        z[k + 1] = __fmul2_rn(z[k + 1], __fmul2_rn(make_float2(d1.y, d1.x), make_float2(r1, r1)));
+    }
+}
+template <int kAct, int P>
+__device__ __forceinline__ void activate_each(float2 (&z)[P]) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+        const float2 d = act_divisor<kAct>(z[k]);
+        z[k] = __fmul2_rn(z[k], make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+    }
+}
+// The activation of z, which sums() makes from the accumulators of a chunk.
+template <int kAct, int P, class Sums>
+__device__ __forceinline__ void activate(float2 (&z)[P], const Sums& sums) {
+    if constexpr (kAct != NVFP4KV_ACT_NONE) {
+        const bool shares = warp_shares<kAct>(z);
+        activate_shared<kAct>(z);
+        if (!shares) {
+            sums();
+            activate_each<kAct>(z);
+        }
+    }
+}
+
+// 2 P tokens' sums of this lane's channel, scaled, with the bias.
+template <int P>
+__device__ __forceinline__ void channel_sums(uint32_t taddr, float2 (&z)[P], float alpha, float bias) {
+    uint32_t v[2 * P];
+    if (P == 8) tmem_ld16(taddr, v);
+    else if (P == 4) tmem_ld8(taddr, v);
+    else tmem_ld4(taddr, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < P; ++k)
+        z[k] = __ffma2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])),
+                          make_float2(alpha, alpha), make_float2(bias, bias));
 }
 
 // Walks down the rows of one channel.  Four addresses take turns, each stepping
@@ -429,31 +491,25 @@ __device__ __forceinline__ void load_residual(const MatmulArgs& a, Walk<const fl
     }
 }
 
-// The next C tokens of one channel, `count` of which exist, from their sums v and
-// residual res, under ch.gate.
+// The next C tokens of one channel, `count` of which exist, from their sums in tensor
+// memory at taddr and residual res, under ch.gate.
 template <int C, int kAct, bool kRes>
-__device__ __forceinline__ void finish_tokens(const MatmulArgs& a, const uint32_t* v, const float* res,
+__device__ __forceinline__ void finish_tokens(const MatmulArgs& a, uint32_t taddr, const float* res,
                                               const Channel& ch, Walk<float>& y, int count) {
+    float2 z[C / 2];
+    const auto sums = [&] { channel_sums(taddr, z, ch.alpha, ch.bias); };
+    sums();
+    activate<kAct>(z, sums);
+    const float2 gg = make_float2(ch.gate, ch.gate);
 #pragma unroll
-    for (int j0 = 0; j0 < C; j0 += 4) {
-        float2 z[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            z[k] = __ffma2_rn(make_float2(__uint_as_float(v[j0 + 2 * k]),
-                                          __uint_as_float(v[j0 + 2 * k + 1])),
-                              make_float2(ch.alpha, ch.alpha), make_float2(ch.bias, ch.bias));
-        act_four<kAct>(z[0], z[1]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int j = j0 + 2 * k;
-            const float2 gg = make_float2(ch.gate, ch.gate);
-            if (kRes) z[k] = __ffma2_rn(z[k], gg, make_float2(res[j], res[j + 1]));
-            else z[k] = __fmul2_rn(z[k], gg);
-            float* y0 = y.row(j, a.ldy);
-            float* y1 = y.row(j + 1, a.ldy);
-            if (j < count) *y0 = z[k].x;
-            if (j + 1 < count) *y1 = z[k].y;
-        }
+    for (int j = 0; j < C; j += 2) {
+        float2& f = z[j / 2];
+        if (kRes) f = __ffma2_rn(f, gg, make_float2(res[j], res[j + 1]));
+        else f = __fmul2_rn(f, gg);
+        float* y0 = y.row(j, a.ldy);
+        float* y1 = y.row(j + 1, a.ldy);
+        if (j < count) *y0 = f.x;
+        if (j + 1 < count) *y1 = f.y;
     }
 }
 
@@ -478,11 +534,8 @@ __device__ __forceinline__ void epilogue_run(const MatmulArgs& a, uint32_t taddr
             for (int j = 0; j < kChunk; ++j) res[j] = next[j];
             load_residual<kChunk>(a, r, next, count - kChunk + here);
         }
-        uint32_t v[kChunk];
         __syncwarp();
-        tmem_ld16(taddr, v);
-        tmem_wait_ld();
-        finish_tokens<kChunk, kAct, kRes>(a, v, res, ch, y, count + here);
+        finish_tokens<kChunk, kAct, kRes>(a, taddr, res, ch, y, count + here);
     }
 }
 
@@ -495,9 +548,6 @@ __device__ __forceinline__ void epilogue_gates(const MatmulArgs& a, uint32_t tad
     const float* r = ch.r;
 #pragma unroll 1
     for (; count > 0; count -= C, taddr += C, m += C) {
-        uint32_t v[C];
-        __syncwarp();
-        tmem_ld4(taddr, v);
         float res[C], g[C];
 #pragma unroll
         for (int j = 0; j < C; ++j) {
@@ -505,13 +555,11 @@ __device__ __forceinline__ void epilogue_gates(const MatmulArgs& a, uint32_t tad
             res[j] = load_plain_if(r + j * a.ldr, here && a.residual);
             g[j] = load_if(a.gate + (size_t)((m + j) / a.rows_per_gate) * a.N + ch.n, here, 0.0f);
         }
-        tmem_wait_ld();
         float2 z[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            z[k] = __ffma2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])),
-                              make_float2(ch.alpha, ch.alpha), make_float2(ch.bias, ch.bias));
-        act_four<kAct>(z[0], z[1]);
+        const auto sums = [&] { channel_sums(taddr, z, ch.alpha, ch.bias); };
+        __syncwarp();
+        sums();
+        activate<kAct>(z, sums);
         const float f[C] = {z[0].x, z[0].y, z[1].x, z[1].y};
 #pragma unroll
         for (int j = 0; j < C; ++j)
@@ -624,9 +672,12 @@ __device__ __forceinline__ void epilogue_pieces(const MatmulArgs& a, uint32_t ta
 #pragma unroll 1
     for (; count > 0; count -= kChunk, skip -= kChunk, taddr += kChunk) {
         uint32_t v[16], res[8];
+        const auto load_sums = [&] {
+            tmem_ld_frag2(taddr, v);
+            tmem_ld_frag2(taddr + (16u << 16), v + 8);
+        };
         __syncwarp();                        // the last chunk's pieces are read and stored
-        tmem_ld_frag2(taddr, v);
-        tmem_ld_frag2(taddr + (16u << 16), v + 8);
+        load_sums();
         if (kRes) {
             sts16(own, next[0]);
             sts16(own + kHalf, next[1]);
@@ -636,30 +687,37 @@ __device__ __forceinline__ void epilogue_pieces(const MatmulArgs& a, uint32_t ta
             ldmatrix4_trans(frag + kHalf, res + 4);
             __syncwarp();
         }
-        tmem_wait_ld();
+        float2 z[8];                         // tokens 8 j .., channels 8 i ..: z[4 j + i]
+        const auto scaled = [&] {
+            tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {        // tokens 8 j ..
-            uint32_t p[4];
-            float2 z[4];                     // channels 8 i ..
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t* s = v + 8 * (i >> 1) + 4 * j + 2 * (i & 1);
-                z[i] = __ffma2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])),
+            for (int k = 0; k < 8; ++k) {
+                const int i = k & 3;
+                const uint32_t* q = v + 8 * (i >> 1) + 4 * (k >> 2) + 2 * (i & 1);
+                z[k] = __ffma2_rn(make_float2(__uint_as_float(q[0]), __uint_as_float(q[1])),
                                   make_float2(alpha, alpha), make_float2(pc.bias[i], pc.bias[i]));
             }
-            act_four<kAct>(z[0], z[1]);
-            act_four<kAct>(z[2], z[3]);
+        };
+        scaled();
+        activate<kAct>(z, [&] {
+            load_sums();
+            scaled();
+        });
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t p[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                float2& f = z[4 * j + i];
                 const float2 g = make_float2(pc.gate[i], pc.gate[i]);
                 if (kRes) {
                     const uint32_t w = res[4 * j + i];
-                    z[i] = __ffma2_rn(z[i], g, make_float2(__uint_as_float(w << 16),
-                                                           __uint_as_float(w & 0xFFFF0000u)));
+                    f = __ffma2_rn(f, g, make_float2(__uint_as_float(w << 16),
+                                                     __uint_as_float(w & 0xFFFF0000u)));
                 } else {
-                    z[i] = __fmul2_rn(z[i], g);
+                    f = __fmul2_rn(f, g);
                 }
-                const __nv_bfloat162 h = __floats2bfloat162_rn(z[i].x, z[i].y);
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
                 p[i] = *reinterpret_cast<const uint32_t*>(&h);
             }
             stmatrix4_trans(frag + j * kHalf, p);
@@ -738,25 +796,16 @@ __device__ __forceinline__ void epilogue_rows(const MatmulArgs& a, uint32_t tadd
     if (kRes && vec) load(0);
 #pragma unroll 1
     for (; count > 0; count -= C, skip -= C, taddr += C) {
-        uint32_t v[C];
+        float2 z[C / 2];
+        const auto sums = [&] { channel_sums(taddr, z, alpha, bias); };
         __syncwarp();                        // the last tokens' rows are read and stored
-        tmem_ld8(taddr, v);
-        tmem_wait_ld();
+        sums();
+        activate<kAct>(z, sums);
 #pragma unroll
-        for (int j = 0; j < C; j += 4) {
-            float2 z[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                z[k] = __ffma2_rn(make_float2(__uint_as_float(v[j + 2 * k]),
-                                              __uint_as_float(v[j + 2 * k + 1])),
-                                  make_float2(alpha, alpha), make_float2(bias, bias));
-            act_four<kAct>(z[0], z[1]);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                z[k] = __fmul2_rn(z[k], make_float2(gate, gate));
-                stage[(j + 2 * k) * 32 + lane] = z[k].x;
-                stage[(j + 2 * k + 1) * 32 + lane] = z[k].y;
-            }
+        for (int k = 0; k < C / 2; ++k) {
+            z[k] = __fmul2_rn(z[k], make_float2(gate, gate));
+            stage[2 * k * 32 + lane] = z[k].x;
+            stage[(2 * k + 1) * 32 + lane] = z[k].y;
         }
         __syncwarp();
         uint2 now[2];

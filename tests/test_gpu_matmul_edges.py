@@ -85,3 +85,62 @@ def test_launches_close_behind_one_another(lib, K):
             c.run()
         assert torch.equal(c.Y, first)
     assert lib.workspace_status(c.ws) == lib.OK
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("how", ["bf16", "rows", "f32", "gates"])
+def test_activations_vanish_far_below_zero(lib, act, how):
+    """SiLU and GELU of z from -130 to 10, channel by channel, and of far larger
+    ones.  With the product zero z is the bias exactly.  Each x = -v log2 e is off by
+    at most two fp32 steps of |x| (one product for SiLU, four for GELU, 2^-24 each,
+    so 2^-22 |x| covers both), which is as much in the logarithm of a tail that is
+    2^-x, on top of 16 steps for the exponential, the reciprocal and the products."""
+    import numpy as np
+    import torch
+    N = 1024 if how != "rows" else 1022
+    bf16 = how != "f32"
+    c = Case(lib, 700, 40, N, 64, w_tiles=False, bf16=bf16, act=act, rpg=3 if how == "gates" else 0)
+    c.X.codes.zero_()
+    if c.gate is not None:
+        c.dev["gate"].fill_(1.0)
+    z = torch.linspace(-130, 10, N)
+    far = torch.tensor([-1e3, -1e4, -1e9, -1e30, -3e38])
+    z[5:5 + far.numel()] = far
+    c.dev["bias"].copy_(z)
+    c.run()
+    torch.cuda.synchronize()
+    got = c.Y.double().cpu().numpy()
+    z = z.numpy().astype(np.float64)
+    v = z if act == "silu" else 2 * np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3)
+    with np.errstate(over="ignore"):
+        want = z / (1 + np.exp(-v))
+    x = np.maximum(-v * np.log2(np.e), 0)
+    # 2^-x below 2^-126 is 0
+    tol = np.abs(want) * np.minimum(x * 2.0 ** -22 + 16 * 2.0 ** -24, 1) + np.abs(z) * 2.0 ** -126
+    if bf16:
+        tol += np.abs(want) * 2.0 ** -8
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= tol).all(), np.abs(got - want).max()
+    below = z < -130.5
+    assert below.sum() == 5 and (got[:, below] == 0).all()
+
+
+@pytest.mark.parametrize("bf16", [True, False], ids=["bf16", "f32"])
+def test_a_channel_shut_off_by_its_bias(lib, bf16):
+    """A bias of -1e9 ends in 0 behind the activation, not in a share of itself that
+    the gate then multiplies; its neighbours stay as they are."""
+    import torch
+    for act in ("silu", "gelu"):
+        c = Case(lib, 710, 50, 80, 128, bf16=bf16, act=act, rpg=20, residual=True)
+        c.bias[3], c.bias[64] = -1e9, -1e30
+        c.dev["bias"].copy_(torch.from_numpy(c.bias))
+        c.run()
+        torch.cuda.synchronize()
+        assert torch.equal(c.Y[:, [3, 64]], c.R[:, [3, 64]])
+        keep = torch.ones(80, dtype=torch.bool)
+        keep[[3, 64]] = False
+        d = Case(lib, 710, 50, 80, 128, bf16=bf16, act=act, rpg=20, residual=True).run()
+        torch.cuda.synchronize()
+        tol = 2.0 ** -7 if bf16 else 2.0 ** -20
+        a, b = c.Y[:, keep].double(), d.Y[:, keep].double()
+        assert bool(((a - b).abs() <= tol * (a.abs() + 1)).all())

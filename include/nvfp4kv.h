@@ -440,6 +440,11 @@ nvfp4kv_status nvfp4kv_grouped_matmul(const nvfp4kv_matrix_view* X, const nvfp4k
                                       const nvfp4kv_epilogue* epilogue, void* Y, long long ldy,
                                       int y_dtype, void* ws, nvfp4kv_stream_t stream);
 
+/* Tokens of a tile that a product of this shape takes on a device of that many
+ * multiprocessors (E = 1: dense): 32, 64, 128, or 192 and 224, which a pair of CTAs
+ * shares.  0 for sizes that the products refuse or fewer than 2 multiprocessors. */
+int nvfp4kv_matmul_tile(int M, int N, int K, int E, int multiprocessors);
+
 /* ------------------------------------------------------------------ de-quantizer */
 
 /*

@@ -113,6 +113,7 @@ def load():
         "nvfp4kv_tensor_scales_from_amax": (st, [vp, vp, vp]),
         "nvfp4kv_chunk_encode": (st, [vp, vp, i32, i32, i32, vp, vp, cv, vp]),
         "nvfp4kv_quantize_matrix": (st, [vp, i32, i32, i32, vp, vp, vp, vp, vp]),
+        "nvfp4kv_matmul_tile": (i32, [i32, i32, i32, i32, i32]),
         "nvfp4kv_matmul": (st, [mv, mv, i32, i32, i32, ep, vp, i64l, i32, vp, vp]),
         "nvfp4kv_grouped_matmul": (st, [mv, mv, i32, i32, i32, i32, vp, ep, vp, i64l, i32, vp,
                                         vp]),
@@ -508,6 +509,12 @@ def grouped_matmul(X: "MatrixBuffer", W: "GroupedMatrixBuffer", offsets, Y, ws, 
     _call_on(device, "nvfp4kv_grouped_matmul", load().nvfp4kv_grouped_matmul, x, w, W.E,
              X.M, W.M, X.N, offsets.data_ptr(), ep, Y.data_ptr(), ldy, y_dtype, ws.data_ptr(),
              stream)
+
+
+def matmul_tile(M, N, K, E=1, multiprocessors=148) -> int:
+    """Tokens of a tile that a product of [M, K] and E matrices [N, K] takes: 32,
+    64, 128, or 192 and 224, which a pair of CTAs shares."""
+    return int(load().nvfp4kv_matmul_tile(M, N, K, E, multiprocessors))
 
 
 def attention_launches(n_chunks, T_c, H, T_q, d=HEAD_DIM) -> int:

@@ -473,6 +473,13 @@ nvfp4kv_status nvfp4kv_grouped_matmul(const nvfp4kv_matrix_view* X, const nvfp4k
     return run_matmul(*X, *W, E, T, N, K, offsets, epilogue, Y, ldy, y_dtype, ws, stream);
 }
 
+int nvfp4kv_matmul_tile(int M, int N, int K, int E, int multiprocessors) {
+    constexpr int kMost = 1 << 24;
+    if (M < 1 || N < 1 || K < 1 || E < 1 || multiprocessors < 2 || M > kMost || N > kMost || K > kMost)
+        return 0;
+    return nvfp4kv::matmul_tile(M, N, K, E, multiprocessors);
+}
+
 nvfp4kv_status nvfp4kv_dequantize(const nvfp4kv_chunk_view* in, int T_c, int H, int d,
                                   void* K_out, void* V_out, int out_dtype,
                                   nvfp4kv_stream_t stream) {

@@ -142,6 +142,8 @@ struct MatmulArgs {
     long long ldr, ldy;
     struct Control* ctl;
 };
+// Tokens a tile (32, 64, 128; 192, 224: a pair of CTAs).
+int matmul_tile(int M, int N, int K, int E, int sms);
 nvfp4kv_status launch_matmul(const MatmulArgs& a, const void* w_codes, const void* x_codes,
                              cudaStream_t stream);
 

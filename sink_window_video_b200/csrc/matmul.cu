@@ -1548,6 +1548,8 @@ nvfp4kv_status launch_any(const MatmulArgs& a, const void* w_codes, const void* 
 
 }  // namespace
 
+int matmul_tile(int M, int N, int K, int E, int sms) { return choose_tile(M, N, K, E, sms); }
+
 nvfp4kv_status launch_matmul(const MatmulArgs& a, const void* w_codes, const void* x_codes,
                              cudaStream_t stream) {
     if (a.offsets)

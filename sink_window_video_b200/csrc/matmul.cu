@@ -1496,15 +1496,18 @@ nvfp4kv_status launch_tn(const MatmulArgs& a, const void* w_codes, const void* x
                : NVFP4KV_ERR_CUDA;
 }
 
-// Tokens a tile (TN) for this product.  Wide tiles read each weight for more
-// tokens, and a pair of CTAs shares them (a step of 256 along k took 0.28 us with
-// 32 tokens, 0.30 with 64, 0.38 with 128, 0.48 with a pair's 192 on [7040, 8192]
-// x [2048, 8192]); narrow ones give more CTAs work and leave a shorter epilogue
-// (about 0.8 us and 25 ns a token) after the last MMA: [333, 1056] x [1001, 1056] took 8.7,
-// 9.3, 10.5 and 15 us with them, [880, 2048] x [2048, 2048] 14.3, 10.2, 8.3 and
-// 9.9; a cluster launch costs 1.2 us (one row: 5.4 us with 64 tokens, 6.7 with a
-// pair).  The rule adds these up in ns and takes the least.  A grouped product's
-// group sizes are not known here: their mean stands for all.
+// Tokens a tile (TN) for this product.  Wide tiles read each weight for more tokens,
+// and a pair of CTAs shares them ([7040, 8192] x [2048, 8192] took 91, 70, 66 and 69
+// us with 64, 128, 192 and 224 tokens, [7266, 2048] over two [2048, 2048] 39, 32, 31
+// and 30); narrow ones give more CTAs work and leave a shorter epilogue (about 0.8 us
+// and 25 ns a token) after the last MMA: [880, 2048] x [2048, 2048] took 11.5, 8.2,
+// 6.8, 9.0 and 9.6 us with 32 to 224 tokens, [200, 4096] x [4096, 4096] 10.8, 8.2, 8.3,
+// 10.4 and 11.4.  A pair costs 1.8 us more to begin and 0.08 us more a step of 256
+// along k, which only more than 128 tokens a tile make up for: one row with K = 512,
+// 2048 and 8192 took 4.1, 5.4 and 9.5 us on single CTAs and 5.9, 7.1 and 13.1 on
+// pairs.  The rule adds these up in ns, as they are on a full device, and takes the
+// least.  A grouped product's group sizes are not known here: their mean stands for
+// all.
 int choose_tile(int M, int N, int K, int E, int sms) {
     const double steps = (K + kStageK - 1) / kStageK;
     int best = 0;
@@ -1515,6 +1518,7 @@ int choose_tile(int M, int N, int K, int E, int sms) {
         // groups of all sizes: half a tile each goes to the ragged end
         const double count = E == 1 ? std::ceil(per / tn) : std::max(1.0, per / tn + 0.5);
         const double size = std::ceil(per / count / 16.0) * 16.0;
+        if (g == 2 && size <= 128.0) continue;
         const double tiles = count * E * ((N + kTileN * g - 1) / (kTileN * g));
         double waves = tiles / (sms / g);
         if (E <= 4 || waves < 1.0) waves = std::ceil(waves);   // many groups even out

@@ -27,3 +27,13 @@ def test_ends_of_the_range():
         for big in [(1 << 24, 1, 32, 1), (1, 1 << 24, 32, 1), (1, 1, 1 << 24, 1), (1, 1, 32, 1024),
                     (1 << 24, 1 << 10, 1 << 10, 1024)]:
             assert swv.matmul_tile(*big, sms) in (32, 64, 128, 192, 224)
+
+
+def test_tiles_of_few_rows_stay_on_single_ctas():
+    """A pair takes longer for a step along k than a CTA does for up to 128 tokens,
+    so that a long K is no reason for one."""
+    for M in (1, 16, 40, 100, 128):
+        for N in (512, 2048, 3696, 8192):
+            for K in (512, 2048, 7808, 8192, 1 << 16):
+                assert swv.matmul_tile(M, N, K) <= 128, (M, N, K)
+                assert swv.matmul_tile(8 * M, N, K, 8) <= 128, (M, N, K)

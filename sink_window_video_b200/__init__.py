@@ -392,7 +392,7 @@ class GroupedMatrixBuffer(_Parts):
     def expert(self, e) -> MatrixBuffer:
         """Matrix e, for quantize_matrix to write."""
         return MatrixBuffer(self.M, self.N, self.mode,
-                            parts=(self.codes[e], self.scales[e], self.tensor_scale[e:e + 1]))
+                            parts=(self.codes[e], self.scales[e], self.tensor_scale[e].view(1)))
 
 
 ACT_NONE, ACT_GELU_TANH, ACT_SILU = 0, 1, 2      # nvfp4kv_activation

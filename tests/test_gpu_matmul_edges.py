@@ -144,3 +144,31 @@ def test_a_channel_shut_off_by_its_bias(lib, bf16):
         tol = 2.0 ** -7 if bf16 else 2.0 ** -20
         a, b = c.Y[:, keep].double(), d.Y[:, keep].double()
         assert bool(((a - b).abs() <= tol * (a.abs() + 1)).all())
+
+
+def test_a_product_reads_the_buffers_as_they_are(lib):
+    """Operands whose storage was replaced in place, copied or moved through a
+    pickle between two products."""
+    import copy
+    import pickle
+
+    import numpy as np
+    import torch
+
+    import matmul_ref as ref
+    c = Case(lib, 720, 70, 144, 256, act="silu").run().check("first")
+    rng = np.random.default_rng(9)
+    c.x = ref.random_matrix(rng, (), 70, 256, False)
+    c.X.codes.set_(torch.from_numpy(c.x["codes"]).cuda())
+    c.X.scales.data = torch.from_numpy(c.x["scales"]).cuda()
+    c.X.tensor_scale = torch.from_numpy(c.x["s"]).cuda()
+    c.run().check("other storage")
+    keep = c.W
+    c.W = pickle.loads(pickle.dumps(keep))
+    c.run().check("pickled")
+    c.W = copy.copy(keep)
+    c.W.codes = torch.zeros_like(keep.codes)
+    assert keep.view.codes == keep.codes.data_ptr()
+    c.W = copy.deepcopy(keep)
+    c.guard.t.copy_(c.before)
+    c.run().check("copied")

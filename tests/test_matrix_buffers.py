@@ -154,3 +154,13 @@ def test_a_view_that_was_handed_out_does_not_change():
     a.codes = a.codes.clone()
     assert a.view.codes == a.codes.data_ptr()
     assert (v.codes, v.scales, v.tensor_scale) == at
+
+
+def test_experts_by_any_index():
+    g = _grouped()
+    for e in (0, 2, -1, -3):
+        m = g.expert(e)
+        assert _addresses(m) == tuple(t[e].data_ptr() for t in (g.codes, g.scales, g.tensor_scale))
+    for e in (3, -4):
+        with pytest.raises(IndexError):
+            g.expert(e)

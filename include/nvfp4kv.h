@@ -398,18 +398,21 @@ typedef struct {
  *   Y[m][n] = residual[m][n] + gate[m / rows_per_gate][n]
  *             * act(s_X s_W sum_k x[m][k] w[n][k] + bias[n]),
  * x, w the decoded codes times their block scales.
- *   X: [M][K], W: [N][K]; each in either block shape.  K a multiple of 32,
- *      and M (N) a multiple of 16 where X (W) is in tiles, else
+ *   X: [M][K], W: [N][K]; each in either block shape.  M, N, K from 1 to 2^24
+ *      and M*K, N*K, M*N up to 2^34, else NVFP4KV_ERR_INVALID_ARG (a product
+ *      without rows too, like an empty matrix or chunk elsewhere).  K a multiple
+ *      of 32, and M (N) a multiple of 16 where X (W) is in tiles, else
  *      NVFP4KV_ERR_UNSUPPORTED.
  *   epilogue: NULL for none.
- *   Y: [M][N] of y_dtype, ldy elements between rows (>= N).  Y may be the
- *      residual itself (same address and stride); other overlaps of the two
- *      are refused with NVFP4KV_ERR_INVALID_ARG.  Y must not overlap the other
- *      inputs.
+ *   Y: [M][N] of y_dtype, ldy elements between rows (>= N, up to 2^40).  Y may
+ *      be the residual itself (same address and stride); other overlaps of the
+ *      two are refused with NVFP4KV_ERR_INVALID_ARG, under different strides any
+ *      of their address ranges.  Y must not overlap the other inputs.
  *   ws: a workspace of at least nvfp4kv_matrix_workspace_bytes(), initialized
  *      once (nvfp4kv_quantize_matrix's serves; only its status word is used).
- * Block products are summed by the tensor core in fp32; the epilogue is fp32;
- * Y is rounded once.  Results do not depend on the stream or the run.  One
+ * Block products are summed by the tensor core in fp32; the epilogue is fp32
+ * (s_X s_W is one fp32 number there: their product has to be one, neither
+ * infinite nor subnormal); Y is rounded once.  Results do not depend on the stream or the run.  One
  * launch; nothing is allocated.
  */
 nvfp4kv_status nvfp4kv_matmul(const nvfp4kv_matrix_view* X, const nvfp4kv_matrix_view* W, int M,

@@ -31,15 +31,13 @@
 // scales (bytes) at (r % 32) * 16 + (r / 32) * 4, which tcgen05.cp
 // (32x128b.warpx4) places in 4 columns of every lane quarter.
 //
-// What bounds it.  [7040, 2048] x [8192, 2048] with GELU to bf16 takes 67 us (3.5
-// PFLOP/s, the bf16 tensor peak is 1.63); without its epilogue 46 us, of which the
-// scale copies (12 tcgen05.cp a stage) are 7; without the MMAs, loads and barriers
-// alone, 33 us.  A pair halves the shared-memory writes and reads of the token
-// tile, which bound the single CTA: 192 tokens take 0.48 us a stage as a pair,
-// 0.52 as one CTA.  Kept busy for 0.3 s the same call takes 82 us: the clock falls
-// to the power limit, and what then counts is energy, the output's above all (50
-// us without the epilogue).  Small calls are latency: one row takes 5.0 us, 3.7
-// from the first CTA's start to the last one's end.
+// What bounds it.  [7040, 2048] x [8192, 2048] with GELU to bf16 takes 69 to 71 us
+// (3.3 to 3.4 PFLOP/s, the bf16 tensor peak is 1.63), without its epilogue 47 us:
+// epilogue and main loop share the SM's shared-memory pipe and issue slots.  A pair
+// halves the shared-memory writes and reads of the token tile, which bound the single
+// CTA ([7040, 8192] x [2048, 8192]: 70 us with 128 tokens on one CTA, 66 with a
+// pair's 192).  Kept busy for seconds the first call takes 87 us: the clock falls to
+// the power limit.  Small calls are latency: one row takes 5.0 to 5.2 us.
 #include <cuda.h>
 
 #include <algorithm>

@@ -445,7 +445,8 @@ nvfp4kv_status nvfp4kv_grouped_matmul(const nvfp4kv_matrix_view* X, const nvfp4k
 
 /* Tokens of a tile that a product of this shape takes on a device of that many
  * multiprocessors (E = 1: dense): 32, 64, 128, or 192 and 224, which a pair of CTAs
- * shares.  0 for sizes that the products refuse or fewer than 2 multiprocessors. */
+ * shares.  0 where M, N or K is outside 1 to 2^24, E below 1 or multiprocessors
+ * below 2. */
 int nvfp4kv_matmul_tile(int M, int N, int K, int E, int multiprocessors);
 
 /* ------------------------------------------------------------------ de-quantizer */
